@@ -12,6 +12,7 @@
  *   - retained-token layer forward/backward, segment-wise gradients
  *                                        Jenga summary §4.1 (Fig. 5), §4.4.2 (Fig. 10)
  *   - block-score predictor              Jenga notes §4.3; Jenga summary §4.3.1 (Fig. 8)
+ *   - dense sub-block operators (layer norm, linear layer, dropout, with gradients)
  *
  * Conventions
  * -----------
@@ -387,6 +388,107 @@ JENGA_API size_t jenga_lm_loss_workspace_bytes(int S, int h, int V, int segment_
 JENGA_API jenga_status jenga_lm_loss_segmented(const void* hidden, const void* w, const int32_t* labels, int S, int h,
                                                int V, int segment_tokens, float* loss, void* dhidden, void* ws,
                                                size_t ws_bytes, jenga_stream_t stream);
+
+/* ------------------------------------------------------------------ dense sub-block operators
+ * Layer norm, linear layer and dropout with their gradients: the pieces of an OPT-style
+ * pre-norm sub-block on retained rows (the pages evaluate OPT next to Llama: Jenga notes, appendix;
+ * the MLP criterion's ReLU form, Jenga summary §4.2.4).  Used in a row: gather ->
+ * jenga_layernorm_fwd -> jenga_linear_fwd (ReLU) -> jenga_linear_fwd -> jenga_dropout (with the
+ * residual) -> scatter, and back.
+ *
+ * Rows.  A call covers `rows` (M) compact rows, a host bound.  n_kept (device int32, nullable)
+ * counts the valid blocks of blk rows: rows at and past *n_kept * blk are neither read nor
+ * written, and add nothing to a reduction; an *n_kept outside [0, rows / blk] is recorded
+ * (JENGA_EINTERNAL) and the call treats no row as valid.  With idx (device int32, ascending block list) compact row r is
+ * sequence row idx[r / blk] * blk + r % blk; an entry that is out of range or not
+ * above the entry before it is recorded and its rows are skipped.  rows must be whole blocks when idx or n_kept is given;
+ * blk is 1 or more and otherwise unused without them.
+ * Pitches (ld*) are in elements.  An output may be the same matrix as an input (same pointer
+ * and pitch) where stated, and must not overlap one otherwise (JENGA_EINVAL).
+ * rows = 0 is a call without work (overwritten gradients become zeros). */
+
+/* jenga_layernorm_fwd -- y[r] = (x[r] - mean) * rstd * gamma + beta per row of h elements, with
+ *   mean = sum x / h, rstd = (sum (x - mean)^2 / h + eps)^(-1/2) in fp32 (centred two-pass).
+ *   x     : F32 / BF16 (dt), [S, h]; with idx the rows are read through the list (no gathered
+ *           copy), else the first `rows` rows.   y: [rows, h] of dt (compact); may be x itself
+ *           without idx.
+ *   gamma, beta : [h] of wdt, nullable (1 and 0).
+ *   mean, rstd  : [rows] fp32 out, nullable; the backward takes them.
+ * Any h up to 16384, any alignment (16-byte aligned rows of a multiple of 16 bytes use 16-byte
+ * accesses).  Errors: EINVAL, EUNSUPPORTED (h). */
+JENGA_API jenga_status jenga_layernorm_fwd(const void* x, int64_t ldx, int S, int h, const int32_t* idx,
+                                           const int32_t* n_kept, int blk, int rows, const void* gamma,
+                                           const void* beta, jenga_dtype wdt, float eps, jenga_dtype dt, void* y,
+                                           int64_t ldy, float* mean, float* rstd, jenga_stream_t stream);
+/* jenga_layernorm_bwd -- gradients of jenga_layernorm_fwd.  With n = (x - mean) rstd, g = dy gamma:
+ *   dx = rstd (g - sum g / h - n sum(g n) / h) (+ dres),  dgamma = sum_r dy n,  dbeta = sum_r dy.
+ *   dy : [rows, h] compact.   x, dres, dx: indexed like the forward's x (sequence rows with
+ *   idx; rows of dx outside the list are not touched).   dres (nullable): gradient of the
+ *   residual branch, added before dx's rounding; dx may be dres, x or (without idx) dy itself.
+ *   dgamma, dbeta: [h] fp32, nullable; added to when accumulate != 0, else overwritten.
+ *   ws: jenga_layernorm_bwd_workspace_bytes(rows, h) bytes when dgamma or dbeta is given.
+ * No atomics: repeated calls on one device give identical bits.  Errors: EINVAL, EWORKSPACE,
+ * EUNSUPPORTED (h). */
+JENGA_API size_t jenga_layernorm_bwd_workspace_bytes(int rows, int h);
+JENGA_API jenga_status jenga_layernorm_bwd(const void* dy, int64_t ldy, const void* x, int64_t ldx, int S, int h,
+                                           const int32_t* idx, const int32_t* n_kept, int blk, int rows,
+                                           const float* mean, const float* rstd, const void* gamma, jenga_dtype wdt,
+                                           const void* dres, int64_t ldr, jenga_dtype dt, void* dx, int64_t ldd,
+                                           float* dgamma, float* dbeta, int accumulate, void* ws, size_t ws_bytes,
+                                           jenga_stream_t stream);
+
+typedef enum {
+  JENGA_ACT_NONE = 0,
+  JENGA_ACT_RELU = 1,
+  JENGA_ACT_GELU = 2, /* exact erf form */
+  JENGA_ACT_SILU = 3,
+} jenga_activation;
+
+/* jenga_linear_fwd -- y = act(x w^T + bias) + residual; one kernel, one rounding of y.
+ *   x: bf16 [M, K];  w: bf16 [N, K];  both with 16-byte aligned rows (pitch a multiple of 8).
+ *   bias: [N] of bias_dt, nullable.   residual: bf16 [M, N], nullable; may be y itself.
+ *   y: bf16 [M, N].   pre: bf16 [M, N] out, nullable: the rounded x w^T + bias, which the
+ *   backward of an activation needs (for ReLU without a residual y itself serves).
+ *   M, N, K: any positive size (K, N <= 2^24).
+ *   ws: jenga_linear_fwd_workspace_bytes(M, N, K) bytes.
+ * Errors: EINVAL, EWORKSPACE. */
+JENGA_API size_t jenga_linear_fwd_workspace_bytes(int M, int N, int K);
+JENGA_API jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                                        jenga_dtype bias_dt, jenga_activation act, const void* residual, int64_t ldr,
+                                        int M, int N, int K, const int32_t* n_kept, int blk, void* y, int64_t ldy,
+                                        void* pre, int64_t ldp, void* ws, size_t ws_bytes, jenga_stream_t stream);
+/* jenga_linear_bwd -- with dz = dy act'(pre):  dx = dz w,  dw = dz^T x,  db = sum_r dz.  (The
+ * residual's gradient is dy itself.)
+ *   dy: bf16 [M, N];  pre: bf16 [M, N] from the forward (ignored for JENGA_ACT_NONE).
+ *   dx: bf16 [M, K], nullable.   dw: fp32 [N, K] (pitch lddw), nullable.   db: fp32 [N], nullable.
+ *   dw and db are added to when accumulate != 0, else overwritten.  x may be null without dw,
+ *   w without dx; the two need 16-byte aligned rows as in the forward.
+ *   ws: jenga_linear_bwd_workspace_bytes(M, N, K, act) bytes (dz, partial sums).
+ * fp32 accumulation, promoted out of the tensor core's accumulator every 1024 rows in dw; dz
+ * enters the products as bf16 (exact for NONE and RELU), as a bf16 hi + lo pair in dw for
+ * GELU and SILU.  No atomics: repeated calls on one device give identical bits.
+ * Errors: EINVAL, EWORKSPACE. */
+JENGA_API size_t jenga_linear_bwd_workspace_bytes(int M, int N, int K, jenga_activation act);
+JENGA_API jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void* x, int64_t ldx, const void* w,
+                                        int64_t ldw, jenga_activation act, const void* pre, int64_t ldp, int M, int N,
+                                        int K, const int32_t* n_kept, int blk, void* dx, int64_t ldd, float* dw,
+                                        int64_t lddw, float* db, int accumulate, void* ws, size_t ws_bytes,
+                                        jenga_stream_t stream);
+
+/* jenga_dropout -- y = keep ? x * 2^16 / (2^16 - T) : 0, plus residual.  Forward and backward are
+ * this call (the backward on the gradient, without a residual): the mask is recomputed, never
+ * stored.  T = floor(p 2^16 + 1/2) (p in [0, 1] is held to 2^-17); an element is kept when its 16
+ * random bits are >= T.  The bits of columns 8 j .. 8 j + 7 at sequence position s are the four
+ * words, low half first, of Philox4x32-10 (Salmon et al., SC'11) with counter (j, s, offset low
+ * word, offset high word) and key (seed low word, seed high word).  s is the sequence row through idx, else
+ * row0 + r: the mask does not depend on which other blocks are kept or on the segmentation.
+ * Use a new offset for every application under one seed (layer, step).
+ *   x, y, residual: F32 / BF16 (dt), [rows, cols] compact; y may be x or residual itself.
+ *   row0 must be 0 with idx; positions stay below 2^31.  Errors: EINVAL. */
+JENGA_API jenga_status jenga_dropout(const void* x, int64_t ldx, const void* residual, int64_t ldr, int rows, int cols,
+                                     const int32_t* idx, const int32_t* n_kept, int blk, int64_t row0, double p,
+                                     uint64_t seed, uint64_t offset, jenga_dtype dt, void* y, int64_t ldy,
+                                     jenga_stream_t stream);
 
 /* ------------------------------------------------------------------ test hook
  * jenga_test_gemm -- C[M, N] = A[M, K] * B[N, K]^T through the tcgen05 GEMM the layer

@@ -1,7 +1,7 @@
 """ctypes declarations of the C ABI in include/jenga.h (argument marshalling only)."""
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libjenga.so")
@@ -18,6 +18,7 @@ STATUS = {0: "JENGA_OK", 1: "JENGA_EINVAL", 2: "JENGA_EUNSUPPORTED", 3: "JENGA_E
 EINVAL, EUNSUPPORTED, ECUDA, ETIMEOUT, EWORKSPACE, EINTERNAL = 1, 2, 3, 4, 5, 6
 F32, BF16 = 0, 1
 SCORE_SOFTMAX_MASS, SCORE_PAPER_BLOCKMAX = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
 SELECT_MEAN_GE, SELECT_TOPK_FRAC, SELECT_ABS_GE, SELECT_TOPK = 0, 1, 2, 3
 
 
@@ -97,6 +98,22 @@ _SIGS = {
                                         c_void_p, c_size_t, c_void_p]),
     "jenga_predict_blocks": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                      c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "jenga_layernorm_fwd": (c_int, [c_void_p, c_int64, c_int, c_int, c_void_p, c_void_p, c_int, c_int, c_void_p,
+                                    c_void_p, c_int, c_float, c_int, c_void_p, c_int64, c_void_p, c_void_p, c_void_p]),
+    "jenga_layernorm_bwd_workspace_bytes": (c_size_t, [c_int, c_int]),
+    "jenga_layernorm_bwd": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_void_p, c_void_p, c_int,
+                                    c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int64, c_int, c_void_p,
+                                    c_int64, c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "jenga_linear_fwd_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
+    "jenga_linear_fwd": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int, c_int, c_void_p, c_int64,
+                                 c_int, c_int, c_int, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                 c_size_t, c_void_p]),
+    "jenga_linear_bwd_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "jenga_linear_bwd": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int, c_void_p, c_int64,
+                                 c_int, c_int, c_int, c_void_p, c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                 c_int, c_void_p, c_size_t, c_void_p]),
+    "jenga_dropout": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_void_p, c_void_p, c_int, c_int64,
+                              c_double, c_uint64, c_uint64, c_int, c_void_p, c_int64, c_void_p]),
     "jenga_test_gemm": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_int, c_void_p, c_int64, c_int,
                                 c_int, c_void_p]),
     "jenga_test_exp2": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_void_p]),

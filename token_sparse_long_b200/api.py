@@ -13,6 +13,8 @@ SCORE_MODES = {"softmax_mass": _lib.SCORE_SOFTMAX_MASS, "paper_blockmax": _lib.S
 SELECT_MODES = {"mean_ge": _lib.SELECT_MEAN_GE, "topk_frac": _lib.SELECT_TOPK_FRAC, "abs_ge": _lib.SELECT_ABS_GE,
                 "topk": _lib.SELECT_TOPK}
 
+ACTIVATIONS = {"none": _lib.ACT_NONE, "relu": _lib.ACT_RELU, "gelu": _lib.ACT_GELU, "silu": _lib.ACT_SILU}
+
 
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
@@ -360,6 +362,218 @@ def jenga_lm_loss_segmented(hidden, w, labels, segment_tokens=4096, dhidden=None
     check(lib.jenga_lm_loss_segmented(_p(hidden), _p(w), _p(labels), S, h, V, segment_tokens, _p(loss), _p(dhidden),
                                       _p(ws), ws.numel(), _stream(stream)))
     return loss, dhidden
+
+
+# ------------------------------------------------------------------ dense sub-block operators
+class _On:
+    """The device of a call's tensors (all on one) and its stream: outputs and workspaces are
+    allocated under that stream, so the caching allocator reuses them in its order."""
+
+    def __init__(self, stream, *ts):
+        _need_cuda(*ts)
+        self.dev = next(t for t in ts if t is not None).device
+        for t in ts:
+            if t is not None and t.device != self.dev:
+                raise ValueError(f"jenga: tensors on {t.device} and {self.dev}")
+        if stream is not None and stream.device != self.dev:
+            raise ValueError(f"jenga: stream of {stream.device}, tensors on {self.dev}")
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard = torch.cuda.stream(self.stream) if self.stream is not None else torch.cuda.device(self.dev)
+        self.guard.__enter__()
+        self.s = ctypes.c_void_p((self.stream or torch.cuda.current_stream(self.dev)).cuda_stream)
+        return self
+
+    def __exit__(self, *a):
+        return self.guard.__exit__(*a)
+
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.dev)
+
+
+def _mat(t, name, cols=None, rows=None, dtype=None):
+    """A 2-d tensor with contiguous rows; its pitch."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: a matrix with contiguous rows required, got {tuple(t.shape)} strides {t.stride()}")
+    if (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] < rows):
+        raise ValueError(f"{name}: [{'>= ' + str(rows) if rows is not None else '*'}, {cols}] required, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} required, got {t.dtype}")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vec(t, name, n, dtype=None):
+    if t is None:
+        return
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name}: contiguous {dtype if dtype is not None else ''} [{n}] required, got {t.dtype} {tuple(t.shape)}")
+
+
+def _rows_arg(idx, n_kept, blk, n_kept_max, rows):
+    """Rows of a call: n_kept_max blocks with a block list, else `rows`."""
+    for t, name in ((idx, "idx"), (n_kept, "n_kept")):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+            raise ValueError(f"{name}: contiguous int32 required")
+    if idx is None:
+        return rows
+    n = idx.numel() if n_kept_max is None else int(n_kept_max)
+    if n < 0 or n > idx.numel():
+        raise ValueError(f"n_kept_max {n} of a list of {idx.numel()}")
+    return n * int(blk)
+
+
+def jenga_layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, idx=None, n_kept=None, blk=1, n_kept_max=None, out=None,
+                        mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of x [S, h] (fp32 / bf16), or of the kept blocks' rows with idx
+    (n_kept_max blocks of blk rows, default all of idx) -> (y [rows, h], mean, rstd fp32 [rows]).
+
+    gamma, beta: [h] fp32 or bf16 (both alike), optional.  n_kept: device int32 count of valid
+    blocks; rows past it stay as they are in the outputs."""
+    with _On(stream, x, gamma, beta, idx, n_kept, out, mean, rstd) as on:
+        S, h = x.shape
+        ldx = _mat(x, "x")
+        rows = _rows_arg(idx, n_kept, blk, n_kept_max, S)
+        _vec(gamma, "gamma", h)
+        _vec(beta, "beta", h)
+        if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+            raise TypeError("gamma and beta differ in dtype")
+        w = gamma if gamma is not None else beta
+        y = on.empty((rows, h), x.dtype) if out is None else out
+        mean = on.empty(rows, torch.float32) if mean is None else mean
+        rstd = on.empty(rows, torch.float32) if rstd is None else rstd
+        ldy = _mat(y, "out", h, rows, x.dtype)
+        _vec(mean, "mean", rows, torch.float32)
+        _vec(rstd, "rstd", rows, torch.float32)
+        check(load().jenga_layernorm_fwd(_p(x), ldx, S, h, _p(idx), _p(n_kept), int(blk), rows, _p(gamma), _p(beta),
+                                         _dt(w) if w is not None else F32, float(eps), _dt(x), _p(y), ldy, _p(mean),
+                                         _p(rstd), on.s))
+    return y, mean, rstd
+
+
+def jenga_layernorm_bwd(dy, x, mean, rstd, gamma=None, idx=None, n_kept=None, blk=1, n_kept_max=None, dres=None,
+                        dx=None, dgamma=None, dbeta=None, accumulate=False, weight_grads=True, ws=None, stream=None):
+    """Gradients of jenga_layernorm_fwd: dy [rows, h] compact; x, dres and dx like the forward's x
+    -> (dx, dgamma fp32 [h], dbeta fp32 [h]).
+
+    dres: gradient of the residual branch, added into dx (dx may be dres: in place).  With idx
+    and no dx given, rows outside the list are zero.  accumulate: add into the given dgamma and
+    dbeta.  weight_grads=False skips both (None unless given)."""
+    with _On(stream, dy, x, mean, rstd, gamma, idx, n_kept, dres, dx, dgamma, dbeta, ws) as on:
+        S, h = x.shape
+        ldx = _mat(x, "x")
+        rows = _rows_arg(idx, n_kept, blk, n_kept_max, S)
+        ldy = _mat(dy, "dy", h, rows, x.dtype)
+        _vec(gamma, "gamma", h)
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            _vec(t, name, rows, torch.float32)
+        if dx is None:
+            dx = on.empty((S, h), x.dtype) if idx is None else torch.zeros(S, h, dtype=x.dtype, device=x.device)
+        ldd = _mat(dx, "dx", h, S, x.dtype)
+        ldr = _mat(dres, "dres", h, S, x.dtype) if dres is not None else 0
+        if weight_grads:
+            if accumulate and (dgamma is None or dbeta is None):
+                raise ValueError("accumulate needs dgamma and dbeta")
+            dgamma = on.empty(h, torch.float32) if dgamma is None else dgamma
+            dbeta = on.empty(h, torch.float32) if dbeta is None else dbeta
+        _vec(dgamma, "dgamma", h, torch.float32)
+        _vec(dbeta, "dbeta", h, torch.float32)
+        lib = load()
+        if ws is None and (dgamma is not None or dbeta is not None):
+            ws = on.empty(lib.jenga_layernorm_bwd_workspace_bytes(rows, h), torch.uint8)
+        check(lib.jenga_layernorm_bwd(_p(dy), ldy, _p(x), ldx, S, h, _p(idx), _p(n_kept), int(blk), rows, _p(mean),
+                                      _p(rstd), _p(gamma), _dt(gamma) if gamma is not None else F32, _p(dres), ldr,
+                                      _dt(x), _p(dx), ldd, _p(dgamma), _p(dbeta), 1 if accumulate else 0, _p(ws),
+                                      ws.numel() if ws is not None else 0, on.s))
+    return dx, dgamma, dbeta
+
+
+def jenga_linear_fwd(x, w, bias=None, act="none", residual=None, n_kept=None, blk=1, out=None, pre=None,
+                     save_pre=False, ws=None, stream=None):
+    """y = act(x w^T + bias) + residual: x [M, K], w [N, K], residual [M, N] bf16, bias [N] fp32 or
+    bf16 -> (y [M, N] bf16, pre [M, N] bf16 or None).
+
+    act: "none", "relu", "gelu" (erf) or "silu".  save_pre (or a given pre) keeps x w^T + bias for
+    the backward.  n_kept: device int32 count of valid blocks of blk rows; later rows of the
+    outputs stay as they are."""
+    bf = torch.bfloat16
+    with _On(stream, x, w, bias, residual, n_kept, out, pre, ws) as on:
+        ldx = _mat(x, "x", dtype=bf)
+        M, K = x.shape
+        ldw = _mat(w, "w", K, dtype=bf)
+        N = w.shape[0]
+        _rows_arg(None, n_kept, blk, None, M)
+        _vec(bias, "bias", N)
+        ldr = _mat(residual, "residual", N, M, bf) if residual is not None else 0
+        y = on.empty((M, N), bf) if out is None else out
+        ldy = _mat(y, "out", N, M, bf)
+        if pre is None and save_pre:
+            pre = on.empty((M, N), bf)
+        ldp = _mat(pre, "pre", N, M, bf) if pre is not None else 0
+        lib = load()
+        if ws is None:
+            ws = on.empty(max(lib.jenga_linear_fwd_workspace_bytes(M, N, K), 1), torch.uint8)
+        check(lib.jenga_linear_fwd(_p(x), ldx, _p(w), ldw, _p(bias), _dt(bias) if bias is not None else F32,
+                                   ACTIVATIONS[act], _p(residual), ldr, M, N, K, _p(n_kept), int(blk), _p(y), ldy,
+                                   _p(pre), ldp, _p(ws), ws.numel(), on.s))
+    return y, pre
+
+
+def jenga_linear_bwd(dy, x, w, act="none", pre=None, n_kept=None, blk=1, need=("dx", "dw", "db"), dx=None, dw=None,
+                     db=None, accumulate=False, ws=None, stream=None):
+    """Gradients of jenga_linear_fwd: dy [M, N], x [M, K], w [N, K], pre [M, N] bf16 ->
+    (dx [M, K] bf16, dw [N, K] fp32, db [N] fp32), None for what `need` leaves out.
+
+    accumulate: add into the given dw and db.  The residual's gradient is dy itself."""
+    bf = torch.bfloat16
+    with _On(stream, dy, x, w, pre, n_kept, dx, dw, db, ws) as on:
+        ldx, ldw = _mat(x, "x", dtype=bf), _mat(w, "w", x.shape[1], dtype=bf)
+        M, K = x.shape
+        N = w.shape[0]
+        ldy = _mat(dy, "dy", N, M, bf)
+        _rows_arg(None, n_kept, blk, None, M)
+        if act != "none" and pre is None:
+            raise ValueError(f"the gradient of {act} needs pre")
+        ldp = _mat(pre, "pre", N, M, bf) if pre is not None else 0
+        if accumulate and (("dw" in need and dw is None) or ("db" in need and db is None)):
+            raise ValueError("accumulate needs dw and db")
+        dx = (on.empty((M, K), bf) if dx is None else dx) if "dx" in need else None
+        dw = (on.empty((N, K), torch.float32) if dw is None else dw) if "dw" in need else None
+        db = (on.empty(N, torch.float32) if db is None else db) if "db" in need else None
+        ldd = _mat(dx, "dx", K, M, bf) if dx is not None else 0
+        lddw = _mat(dw, "dw", K, N, torch.float32) if dw is not None else 0
+        _vec(db, "db", N, torch.float32)
+        lib = load()
+        if ws is None:
+            ws = on.empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, ACTIVATIONS[act]), torch.uint8)
+        check(lib.jenga_linear_bwd(_p(dy), ldy, _p(x), ldx, _p(w), ldw, ACTIVATIONS[act], _p(pre), ldp, M, N, K,
+                                   _p(n_kept), int(blk), _p(dx), ldd, _p(dw), lddw, _p(db), 1 if accumulate else 0,
+                                   _p(ws), ws.numel(), on.s))
+    return dx, dw, db
+
+
+def jenga_dropout(x, p, seed, offset=0, residual=None, idx=None, n_kept=None, blk=1, row0=0, out=None, stream=None):
+    """y = keep ? x / (1 - p) : 0, plus residual, for x [rows, cols] fp32 / bf16 (compact rows).
+
+    The mask is a function of (seed, offset, sequence position, column) -- recomputed, never
+    stored -- with positions row0 + r, or the block list's rows with idx.  The backward is the
+    same call on the gradient, without the residual.  out may be x or residual (in place)."""
+    with _On(stream, x, residual, idx, n_kept, out) as on:
+        ldx = _mat(x, "x")
+        rows, cols = x.shape
+        _rows_arg(None, n_kept, blk, None, rows)
+        if idx is not None:
+            if idx.dtype != torch.int32 or not idx.is_contiguous() or idx.numel() * blk < rows:
+                raise ValueError("idx: contiguous int32 list of every row's block required")
+        ldr = _mat(residual, "residual", cols, rows, x.dtype) if residual is not None else 0
+        y = on.empty((rows, cols), x.dtype) if out is None else out
+        ldy = _mat(y, "out", cols, rows, x.dtype)
+        m64 = (1 << 64) - 1
+        check(load().jenga_dropout(_p(x), ldx, _p(residual), ldr, rows, cols, _p(idx), _p(n_kept), int(blk), int(row0),
+                                   float(p), int(seed) & m64, int(offset) & m64, _dt(x), _p(y), ldy, on.s))
+    return y
 
 
 def jenga_test_gemm(a, b, out_f32=True, bn=256, stream=None):

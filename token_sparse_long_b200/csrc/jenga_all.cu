@@ -10,3 +10,6 @@
 #include "lm_loss.cu"
 #include "predictor.cu"
 #include "score_noalloc.cu"
+#include "layernorm.cu"
+#include "dropout.cu"
+#include "linear.cu"

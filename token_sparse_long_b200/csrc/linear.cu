@@ -1,0 +1,366 @@
+// Linear layer with bias, activation and residual in the product's epilogue, and its
+// gradients: the dense pieces of an OPT-style feed-forward sub-block on retained rows (the
+// Llama layer's projections are fused in layer.cu).
+//
+//   z = x w^T + bias,   y = act(z) + residual,   pre = z (kept for the backward, bf16)
+//   dz = dy act'(pre),  dx = dz w,   dw (+)= dz^T x,   db (+)= sum_r dz
+//
+// bf16 operands, fp32 accumulation; z stays fp32 up to y's one rounding.  dz is rounded to bf16
+// to be a tensor-core operand: exact for no activation and ReLU (dy or 0).  For GELU and
+// SiLU the rounding (half a bf16 step, 2^-8 relative) is below that of the bf16 result in dx; the
+// fp32 dw takes dz as a (hi, lo) bf16 pair in two passes over the rows, which keeps 16 bits.
+// db sums dz in fp32 before any rounding.
+#include "linear_tc.cuh"
+
+namespace jenga {
+
+// dz = dy act'(pre) as bf16 (hi, and lo = bf16(dz - hi)), and partial column sums of dz:
+// CTA (strip, chunk) takes 256 columns x the chunk's rows, eight columns per lane, one row per
+// warp at a time; the eight warps' sums are added in order, part[chunk][N].  Rows from the
+// valid count up to the next multiple of 64 are written as zeros (the product over the rows
+// reads whole 64-row blocks).  VEC: rows of dy and pre are 16-byte aligned.
+template <bool VEC, bool WRITE, bool LO>
+__global__ void __launch_bounds__(256)
+    linear_dz_kernel(const bf16* __restrict__ dy, int64_t ldy, const bf16* __restrict__ pre, int64_t ldp, int act,
+                     int M, int N, const int32_t* n_kept, int blk, int rows_per, bf16* __restrict__ hi,
+                     bf16* __restrict__ lo, int64_t ldz, float* __restrict__ part) {
+  __shared__ float s_sum[8][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int valid = valid_rows(RowMap{nullptr, n_kept, blk, 0, M});
+  const int c = blockIdx.x * 256 + lane * 8;
+  const int r_lo = blockIdx.y * rows_per;
+  const int r_hi = min(min((valid + 63) / 64 * 64, M), r_lo + rows_per);
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  if (c < N) {
+#pragma unroll 2
+    for (int r = r_lo + warp; r < r_hi; r += 8) {
+      float d[8], z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        d[e] = 0.f;
+        z[e] = 0.f;
+      }
+      if (r < valid) {
+        if (VEC && c + 8 <= N) {
+          RowVec<bf16, 8> a;
+          a.load(dy + (int64_t)r * ldy + c);
+          if (act != JENGA_ACT_NONE) {
+            RowVec<bf16, 8> b;
+            b.load(pre + (int64_t)r * ldp + c);
+            b.get(z);
+          }
+          a.get(d);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (c + e < N) {
+              d[e] = __bfloat162float(dy[(int64_t)r * ldy + c + e]);
+              if (act != JENGA_ACT_NONE) z[e] = __bfloat162float(pre[(int64_t)r * ldp + c + e]);
+            }
+          }
+        }
+        if (act == JENGA_ACT_RELU) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] = z[e] > 0.f ? d[e] : 0.f;
+        } else if (act != JENGA_ACT_NONE) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] *= act_slope(z[e], act);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += d[e];
+      }
+      if (WRITE) {  // the pitch is a multiple of 8: a vector may reach into the padding
+        RowVec<bf16, 8>::store(hi + (int64_t)r * ldz + c, d);
+        if (LO) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[e] -= __bfloat162float(__float2bfloat16_rn(d[e]));
+          RowVec<bf16, 8>::store(lo + (int64_t)r * ldz + c, d);
+        }
+      }
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s_sum[warp][lane * 8 + e] = sum[e];
+  __syncthreads();
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col < N) {
+    float a = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) a += s_sum[w][threadIdx.x];
+    part[(int64_t)blockIdx.y * N + col] = a;
+  }
+}
+
+// db[c] (+)= sum over the chunks, in order
+__global__ void __launch_bounds__(128) linear_db_reduce_kernel(const float* __restrict__ part, int chunks, int N,
+                                                               float* db, int accumulate) {
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (c >= N) return;
+  float a = 0.f;
+  for (int p = 0; p < chunks; ++p) a += part[(int64_t)p * N + c];
+  db[c] = accumulate ? db[c] + a : a;
+}
+
+// The rows of x past the last whole 64-row block, with zeros up to 64 rows (a device row count
+// can end inside x, whose later rows may hold anything).
+__global__ void __launch_bounds__(256) linear_tail_kernel(const bf16* __restrict__ x, int64_t ldx, int M, int K,
+                                                          const int32_t* n_kept, int blk, bf16* __restrict__ tail,
+                                                          int64_t ldt) {
+  const int valid = valid_rows(RowMap{nullptr, n_kept, blk, 0, M});
+  const int r0 = valid / 64 * 64, r = blockIdx.y;
+  for (int c = blockIdx.x * 256 + threadIdx.x; c < K; c += gridDim.x * 256)
+    tail[r * ldt + c] = r0 + r < valid ? x[(int64_t)(r0 + r) * ldx + c] : __float2bfloat16_rn(0.f);
+}
+
+// ------------------------------------------------------------------ host
+struct LinMats {
+  CUtensorMap a, a2, b, tail, out, pre;
+};
+
+template <int BN, bool AMN, bool BMN, int MODE>
+static jenga_status linear_launch(const LinMats& m, const LinArgs& p, const char* name, cudaStream_t st) {
+  using L = LinSmem<BN>;
+  auto kernel = linear_tc_kernel<BN, AMN, BMN, MODE>;
+  JENGA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL));
+  const int64_t tiles = (int64_t)((p.R + 255) / 256) * ((p.C + BN - 1) / BN);
+  const int pairs = sm_count() / 2;
+  const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
+  const int ps = prof_begin(name, st);
+  kernel<<<grid, LT_THREADS, L::TOTAL, st>>>(m.a, m.a2, m.b, m.tail, m.out, m.pre, p);
+  prof_end(ps, st);
+  JENGA_LAUNCH_CHECK();
+  return JENGA_OK;
+}
+
+// bf16 tensor map for an output of 32-row tiles; false when the matrix is not 16-byte aligned
+static bool out_map(CUtensorMap* map, const void* base, int rows, int cols, int64_t ld) {
+  return base && is16(base) && ld % 8 == 0 && make_tmap_bf16(map, base, rows, cols, ld, 32) == JENGA_OK;
+}
+
+static bool lin_operand_ok(const void* p, int64_t ld) { return is16(p) && ld % 8 == 0; }
+
+static int dz_rows_per(int M, int N) {  // rows per chunk of linear_dz: about four CTAs an SM, whole 64-row blocks
+  const int strips = (N + 255) / 256;
+  int chunks = (4 * sm_count() + strips - 1) / strips;
+  int per = (M + chunks - 1) / chunks;
+  per = (per + 63) / 64 * 64;
+  return per;
+}
+
+struct LinBwdWs {
+  bf16 *hi, *lo, *tail;
+  float* part;
+  int64_t ldz, ldt;
+  size_t bytes;
+};
+static LinBwdWs lin_bwd_carve(void* ws, int M, int N, int K, int act) {
+  LinBwdWs w;
+  w.ldz = (N + 7) / 8 * 8;
+  w.ldt = (K + 7) / 8 * 8;
+  Carve c(ws);
+  w.hi = c.take<bf16>((size_t)M * w.ldz);
+  w.lo = act == JENGA_ACT_GELU || act == JENGA_ACT_SILU ? c.take<bf16>((size_t)M * w.ldz) : nullptr;
+  w.tail = c.take<bf16>((size_t)64 * w.ldt);
+  const int per = dz_rows_per(M, N);
+  w.part = c.take<float>((size_t)((M + per - 1) / per) * N);
+  w.bytes = c.used();
+  return w;
+}
+
+static jenga_status lin_check(const char* who, int M, int N, int K, const int32_t* n_kept, int blk, int act) {
+  JENGA_CHECK_ARG(M >= 0 && N >= 1 && K >= 1 && blk >= 1, "%s: bad sizes M=%d N=%d K=%d blk=%d", who, M, N, K, blk);
+  JENGA_CHECK_ARG(M <= (1 << 30) && N <= (1 << 24) && K <= (1 << 24), "%s: sizes too large M=%d N=%d K=%d", who, M, N,
+                  K);
+  JENGA_CHECK_ARG(!n_kept || M % blk == 0, "%s: M (%d) must be whole blocks of %d", who, M, blk);
+  JENGA_CHECK_ARG(act >= JENGA_ACT_NONE && act <= JENGA_ACT_SILU, "%s: activation %d", who, act);
+  return JENGA_OK;
+}
+
+}  // namespace jenga
+
+using namespace jenga;
+
+extern "C" size_t jenga_linear_fwd_workspace_bytes(int M, int N, int K) {
+  (void)M;
+  (void)N;
+  (void)K;
+  return 0;
+}
+
+extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                                         jenga_dtype bias_dt, jenga_activation act, const void* residual, int64_t ldr,
+                                         int M, int N, int K, const int32_t* n_kept, int blk, void* y, int64_t ldy,
+                                         void* pre, int64_t ldp, void* ws, size_t ws_bytes, jenga_stream_t stream) {
+  JENGA_TRY(lin_check("jenga_linear_fwd", M, N, K, n_kept, blk, act));
+  JENGA_CHECK_ARG(bias_dt == JENGA_F32 || bias_dt == JENGA_BF16, "jenga_linear_fwd: bias dtype");
+  JENGA_CHECK_ARG(ldx >= K && ldw >= K && ldy >= N && (!residual || ldr >= N) && (!pre || ldp >= N),
+                  "jenga_linear_fwd: row pitch smaller than the row");
+  if (M == 0) return JENGA_OK;
+  JENGA_CHECK_ARG(x && w && y, "jenga_linear_fwd: null pointer");
+  JENGA_CHECK_ARG(lin_operand_ok(x, ldx) && lin_operand_ok(w, ldw),
+                  "jenga_linear_fwd: x and w need 16-byte aligned rows (pitch a multiple of 8)");
+  const uint64_t ny = span_bytes(M, N, ldy, 2), np = span_bytes(M, N, ldp, 2), nx = span_bytes(M, K, ldx, 2),
+                 nw = span_bytes(N, K, ldw, 2), nr = span_bytes(M, N, ldr, 2);
+  JENGA_CHECK_ARG(alias_ok(y, ldy, ny, x, ldx, nx, false) && alias_ok(y, ldy, ny, w, ldw, nw, false) &&
+                      alias_ok(y, ldy, ny, residual, ldr, nr, true) && alias_ok(y, ldy, ny, pre, ldp, np, false) &&
+                      alias_ok(pre, ldp, np, x, ldx, nx, false) && alias_ok(pre, ldp, np, w, ldw, nw, false) &&
+                      alias_ok(pre, ldp, np, residual, ldr, nr, false),
+                  "jenga_linear_fwd: an output overlaps an input (only y = residual, the same matrix, is allowed)");
+  (void)ws;
+  (void)ws_bytes;
+  cudaStream_t st = (cudaStream_t)stream;
+  LinArgs p{};
+  p.R = M;
+  p.C = N;
+  p.m = M;
+  p.nkb = (K + 63) / 64;
+  p.passes = 1;
+  p.n_kept = n_kept;
+  p.blk = blk;
+  p.bias = bias;
+  p.bias_bf16 = bias_dt == JENGA_BF16;
+  p.act = act;
+  p.residual = (const bf16*)residual;
+  p.ldr = ldr;
+  p.out = y;
+  p.ldo = ldy;
+  p.pre = (bf16*)pre;
+  p.ldp = ldp;
+  LinMats m;
+  JENGA_TRY(make_tmap_bf16(&m.a, x, M, K, ldx, 128));
+  const int64_t t256 = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
+  const bool wide = t256 >= sm_count() / 2;
+  JENGA_TRY(make_tmap_bf16(&m.b, w, N, K, ldw, wide ? 128 : 64));
+  m.a2 = m.tail = m.out = m.pre = m.a;
+  p.out_tma = out_map(&m.out, y, M, N, ldy);
+  p.pre_tma = out_map(&m.pre, pre, M, N, ldp);
+  return wide ? linear_launch<256, false, false, LIN_OUT>(m, p, "linear_fwd", st)
+              : linear_launch<128, false, false, LIN_OUT>(m, p, "linear_fwd", st);
+}
+
+extern "C" size_t jenga_linear_bwd_workspace_bytes(int M, int N, int K, jenga_activation act) {
+  if (M < 1 || N < 1 || K < 1) return 0;
+  return lin_bwd_carve(nullptr, M, N, K, act).bytes;
+}
+
+extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void* x, int64_t ldx, const void* w,
+                                         int64_t ldw, jenga_activation act, const void* pre, int64_t ldp, int M, int N,
+                                         int K, const int32_t* n_kept, int blk, void* dx, int64_t ldd, float* dw,
+                                         int64_t lddw, float* db, int accumulate, void* ws, size_t ws_bytes,
+                                         jenga_stream_t stream) {
+  JENGA_TRY(lin_check("jenga_linear_bwd", M, N, K, n_kept, blk, act));
+  JENGA_CHECK_ARG(ldy >= N && (!dw || (ldx >= K && lddw >= K)) && (!dx || (ldw >= K && ldd >= K)) &&
+                      (act == JENGA_ACT_NONE || ldp >= N),
+                  "jenga_linear_bwd: row pitch smaller than the row");
+  cudaStream_t st = (cudaStream_t)stream;
+  if (M == 0) {  // empty sums
+    if (!accumulate && dw)
+      JENGA_CUDA_TRY(cudaMemset2DAsync(dw, (size_t)lddw * 4, 0, (size_t)K * 4, (size_t)N, st));
+    if (!accumulate && db) JENGA_CUDA_TRY(cudaMemsetAsync(db, 0, (size_t)N * 4, st));
+    return JENGA_OK;
+  }
+  JENGA_CHECK_ARG(dy && (act == JENGA_ACT_NONE || pre) && (!dw || x) && (!dx || w), "jenga_linear_bwd: null pointer");
+  if (!dx && !dw && !db) return JENGA_OK;
+  JENGA_CHECK_ARG((!dw || lin_operand_ok(x, ldx)) && (!dx || lin_operand_ok(w, ldw)),
+                  "jenga_linear_bwd: x and w need 16-byte aligned rows (pitch a multiple of 8)");
+  if (act == JENGA_ACT_NONE) pre = nullptr;
+  if (!dw) x = nullptr;
+  if (!dx) w = nullptr;
+  const uint64_t nd = span_bytes(M, K, ldd, 2), ndw = span_bytes(N, K, lddw, 4), ndy = span_bytes(M, N, ldy, 2),
+                 np = span_bytes(M, N, ldp, 2), nx = span_bytes(M, K, ldx, 2), nw = span_bytes(N, K, ldw, 2);
+  JENGA_CHECK_ARG(alias_ok(dx, ldd, nd, dy, ldy, ndy, false) && alias_ok(dx, ldd, nd, x, ldx, nx, false) &&
+                      alias_ok(dx, ldd, nd, w, ldw, nw, false) && alias_ok(dx, ldd, nd, pre, ldp, np, false) &&
+                      alias_ok(dw, lddw, ndw, dy, ldy, ndy, false) && alias_ok(dw, lddw, ndw, x, ldx, nx, false) &&
+                      alias_ok(dw, lddw, ndw, w, ldw, nw, false) && alias_ok(dw, lddw, ndw, pre, ldp, np, false),
+                  "jenga_linear_bwd: an output overlaps an input");
+  const size_t need = jenga_linear_bwd_workspace_bytes(M, N, K, act);
+  if (!ws || ws_bytes < need)
+    return fail(JENGA_EWORKSPACE, "jenga_linear_bwd: workspace %zu < %zu", ws ? ws_bytes : (size_t)0, need);
+  const LinBwdWs W = lin_bwd_carve(ws, M, N, K, act);
+  // dy itself is the operand when nothing has to be computed, aligned or cut off at a device count
+  const bool direct = act == JENGA_ACT_NONE && !n_kept && lin_operand_ok(dy, ldy);
+  const bf16* dz = direct ? (const bf16*)dy : W.hi;
+  const int64_t ldz = direct ? ldy : W.ldz;
+  const bool two = W.lo && dw;
+  const int per = dz_rows_per(M, N), chunks = (M + per - 1) / per;
+  if (!direct || db) {
+    float* part = db ? W.part : nullptr;
+    const bool vec = lin_operand_ok(dy, ldy) && (!pre || lin_operand_ok(pre, ldp));
+    const dim3 grid((N + 255) / 256, chunks);
+    auto go = [&](auto kernel) {
+      kernel<<<grid, 256, 0, st>>>((const bf16*)dy, ldy, (const bf16*)pre, ldp, act, M, N, n_kept, blk, per, W.hi, W.lo,
+                                   W.ldz, part);
+    };
+    const int ps = prof_begin("linear_dz", st);
+    if (direct)
+      go(linear_dz_kernel<true, false, false>);
+    else if (vec)
+      two ? go(linear_dz_kernel<true, true, true>) : go(linear_dz_kernel<true, true, false>);
+    else
+      two ? go(linear_dz_kernel<false, true, true>) : go(linear_dz_kernel<false, true, false>);
+    prof_end(ps, st);
+    JENGA_LAUNCH_CHECK();
+    if (db) {
+      const int p2 = prof_begin("linear_db_reduce", st);
+      linear_db_reduce_kernel<<<(N + 127) / 128, 128, 0, st>>>(W.part, chunks, N, db, accumulate);
+      prof_end(p2, st);
+      JENGA_LAUNCH_CHECK();
+    }
+  }
+  const int pairs = sm_count() / 2;
+  if (dx) {
+    LinArgs p{};
+    p.R = M;
+    p.C = K;
+    p.m = M;
+    p.nkb = (N + 63) / 64;
+    p.passes = 1;
+    p.n_kept = n_kept;
+    p.blk = blk;
+    p.out = dx;
+    p.ldo = ldd;
+    LinMats m;
+    JENGA_TRY(make_tmap_bf16(&m.a, dz, M, N, ldz, 128));
+    JENGA_TRY(make_tmap_bf16(&m.b, w, N, K, ldw, 64));
+    m.a2 = m.tail = m.out = m.pre = m.a;
+    p.out_tma = out_map(&m.out, dx, M, K, ldd);
+    const int64_t t256 = (int64_t)((M + 255) / 256) * ((K + 255) / 256);
+    JENGA_TRY((t256 >= pairs ? linear_launch<256, false, true, LIN_OUT>(m, p, "linear_dx", st)
+                             : linear_launch<128, false, true, LIN_OUT>(m, p, "linear_dx", st)));
+  }
+  if (dw) {
+    LinArgs p{};
+    p.R = N;
+    p.C = K;
+    p.m = M;
+    p.nkb = (M + 63) / 64;
+    p.passes = two ? 2 : 1;
+    p.n_kept = n_kept;
+    p.blk = blk;
+    p.out = dw;
+    p.ldo = lddw;
+    p.accumulate = accumulate;
+    p.tail = n_kept != nullptr;
+    LinMats m;
+    JENGA_TRY(make_tmap_bf16(&m.a, dz, M, N, ldz, 64));
+    m.a2 = m.tail = m.out = m.pre = m.a;
+    if (two) JENGA_TRY(make_tmap_bf16(&m.a2, W.lo, M, N, W.ldz, 64));
+    JENGA_TRY(make_tmap_bf16(&m.b, x, M, K, ldx, 64));
+    if (p.tail) {
+      const int ps = prof_begin("linear_tail", st);
+      linear_tail_kernel<<<dim3((K + 1023) / 1024, 64), 256, 0, st>>>((const bf16*)x, ldx, M, K, n_kept, blk, W.tail,
+                                                                      W.ldt);
+      prof_end(ps, st);
+      JENGA_LAUNCH_CHECK();
+      JENGA_TRY(make_tmap_bf16(&m.tail, W.tail, 64, K, W.ldt, 64));
+    }
+    p.out_tma = is16(dw) && lddw % 4 == 0 && make_tmap_f32(&m.out, dw, N, K, lddw, 32) == JENGA_OK;
+    const int64_t t256 = (int64_t)((N + 255) / 256) * ((K + 255) / 256);
+    JENGA_TRY((t256 >= pairs ? linear_launch<256, true, true, LIN_GRAD>(m, p, "linear_dw", st)
+                             : linear_launch<128, true, true, LIN_GRAD>(m, p, "linear_dw", st)));
+  }
+  return JENGA_OK;
+}

@@ -1,0 +1,473 @@
+// tcgen05 matrix products of the linear layer (sm_100a), on CTA pairs.
+//
+//   D[R, C] = sum_k A[R, k] B[C, k]        bf16 in, fp32 accumulate
+//
+// Three products share the kernel; an operand whose reduction index is its slow (row) index in
+// memory is taken MN-major, straight from the row-major matrix (no transposed copy):
+//   forward   y  = x w^T    A = x  [M, K]  K-major,   B = w [N, K]  K-major
+//   dx        dx = dz w     A = dz [M, N]  K-major,   B = w [N, K]  MN-major (reduction N)
+//   dw        dw = dz^T x   A = dz [M, N]  MN-major,  B = x [M, K]  MN-major (reduction M)
+//
+// A cluster of two CTAs owns a 256 x BN tile: each CTA stages its 128 rows of A and half of
+// B's rows per 64-deep k-block, and one tcgen05.mma (cta_group::2, M 256) issued by the
+// leader reads both CTAs' shared memory, so each SM moves half of the B tile it would alone.
+// Accumulators (128 lanes x BN columns per CTA) are double buffered in tensor memory.
+// 320 threads per CTA:
+//   warp 0      TMA producer (both CTAs; completion counted on the leader's full barrier)
+//   warp 1      allocates tensor memory; in the leader one lane issues the MMAs and commits
+//               (multicast to both CTAs' barriers)
+//   warps 2..9  epilogue: two warps per TMEM lane quarter, half of the columns each
+// Persistent: one cluster per SM pair walks the tiles in bands of 8 row tiles (row tile
+// fastest), so that a wave's operands stay within L2.
+#pragma once
+
+#include "gemm_tc.cuh"
+#include "rows.cuh"
+
+namespace jenga {
+
+constexpr int LT_THREADS = 320;
+constexpr int LT_BAND = 8;
+
+enum LinMode : int {
+  LIN_OUT = 0,   // out bf16 = act(acc + bias) (+ residual); pre bf16 = acc + bias
+  LIN_GRAD = 1,  // out fp32 (+)= acc, the accumulator promoted every LT_CHUNK k-blocks
+};
+
+// k-blocks (of 64) that a tensor-memory accumulator sums before it is added into fp32
+// registers.  The tensor core truncates when it adds into the accumulator: measured relative
+// loss 4e-6 over 4096 products and 3e-5 over 26240 (1e-4 for all-positive operands), growing
+// with the length.  1024 products at a time keep it near 1e-6 whatever the number of rows.
+constexpr int LT_CHUNK = 16;
+
+struct LinArgs {
+  int R, C, nkb;                  // rows, columns, k-blocks of one pass over the reduction
+  int m;                          // host bound on the rows of x (R, or the reduction of LIN_GRAD)
+  int passes;                     // LIN_GRAD: 2 = A is a (hi, lo) pair summed over two passes
+  const int32_t* n_kept;          // device count of valid blocks of x's rows (nullable)
+  int blk;
+  const void* bias;
+  int bias_bf16, act;
+  const bf16* residual;
+  int64_t ldr;
+  void* out;
+  int64_t ldo;
+  bf16* pre;
+  int64_t ldp;
+  int out_tma, pre_tma;           // the tensor maps of out / pre are valid
+  int accumulate;                 // LIN_GRAD
+  int tail;                       // LIN_GRAD: the last partial k-block comes from the tail copy of x
+};
+
+template <int BN>
+struct LinSmem {
+  static constexpr int STAGES = 5;
+  static constexpr int A_BYTES = 128 * 64 * 2;
+  static constexpr int B_BYTES = BN / 2 * 64 * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STG_OFF = STAGES * STAGE_BYTES;
+  static constexpr int STG_BYTES = 8 * 2 * 4096;  // two 32-row x 128-byte tiles per epilogue warp
+  static constexpr int BAR_OFF = STG_OFF + STG_BYTES;
+  static constexpr int TOTAL = BAR_OFF + 256 + 1024;
+  static_assert(TOTAL <= 232448, "shared memory per CTA");
+};
+
+// ---- CTA-pair PTX
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// shared::cluster address of `addr` (this CTA's shared memory) in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// TMA tile load into this CTA's shared memory, completion counted on a barrier of the pair
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar_cluster, int x,
+                                                 int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on the barrier at this offset in both CTAs once the MMAs issued so far are complete
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_holder, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_holder)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// ---- activations (fp32)
+__device__ __forceinline__ float act_value(float z, int act) {
+  if (act == JENGA_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+  if (act == JENGA_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (act == JENGA_ACT_SILU) return z / (1.f + __expf(-z));
+  return z;
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == JENGA_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if (act == JENGA_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+  if (act == JENGA_ACT_SILU) {
+    const float s = 1.f / (1.f + __expf(-z));
+    return s * (1.f + z * (1.f - s));
+  }
+  return 1.f;
+}
+
+template <int BN, bool AMN, bool BMN, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
+                     const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmTail,
+                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPre, LinArgs p) {
+  using L = LinSmem<BN>;
+  constexpr int ST = L::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+  uint64_t* empty = full + ST;
+  uint64_t* acc_full = empty + ST;     // [2]
+  uint64_t* acc_empty = acc_full + 2;  // [2], used in the leader
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  // LIN_OUT: the valid rows bound the row tiles; LIN_GRAD: they are the reduction
+  const int valid = valid_rows(RowMap{nullptr, p.n_kept, p.blk, 0, p.m});
+  const int rows = MODE == LIN_OUT ? valid : p.R;
+  const int nkb1 = MODE == LIN_OUT ? p.nkb : (valid + 63) / 64;
+  const int nkb = nkb1 * (MODE == LIN_GRAD ? p.passes : 1);
+  const int ntr = (rows + 255) / 256, ntc = (p.C + BN - 1) / BN;
+  const int ntiles = ntr * ntc;
+  if (cluster >= ntiles) return;  // uniform over the cluster
+  auto tile_at = [&](int t, int& r0, int& c0) {
+    const int band = t / (LT_BAND * ntc), rem = t - band * LT_BAND * ntc;
+    const int gm = min(LT_BAND, ntr - band * LT_BAND);
+    r0 = (band * LT_BAND + rem % gm) * 256;
+    c0 = rem / gm * BN;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 16);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_holder, 2 * BN);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    int g = 0;
+    bool ok = true;
+    for (int t = cluster; ok && t < ntiles; t += nclusters) {
+      int r0, c0;
+      tile_at(t, r0, c0);
+      r0 += rank * 128;
+      c0 += rank * (BN / 2);
+      for (int kb = 0; kb < nkb; ++kb, ++g) {
+        const int s = g % ST;
+        if (g >= ST && !mbar_wait(&empty[s], ((g / ST) - 1) & 1, SITE_LINEAR)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + s * L::STAGE_BYTES;
+        uint8_t* sb = sa + L::A_BYTES;
+        const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::STAGE_BYTES);
+        const bool lo = MODE == LIN_GRAD && kb >= nkb1;
+        const int kk = lo ? kb - nkb1 : kb;
+        const CUtensorMap* ma = lo ? &tmA2 : &tmA;
+        if (AMN) {
+          tma_load_2d_pair(sa, ma, bar, r0, kk * 64);
+          tma_load_2d_pair(sa + 8192, ma, bar, r0 + 64, kk * 64);
+        } else {
+          tma_load_2d_pair(sa, ma, bar, kk * 64, r0);
+        }
+        if (BMN) {
+          const bool tl = MODE == LIN_GRAD && p.tail && (kk + 1) * 64 > valid;
+          const CUtensorMap* mb = tl ? &tmTail : &tmB;
+#pragma unroll
+          for (int j = 0; j < BN / 128; ++j)
+            tma_load_2d_pair(sb + j * 8192, mb, bar, c0 + j * 64, tl ? 0 : kk * 64);
+        } else {
+          tma_load_2d_pair(sb, &tmB, bar, kk * 64, c0);
+        }
+      }
+    }
+    // the pair's copies are complete before either CTA leaves (at once after a normal run: the
+    // MMAs waited for the same phases)
+    if (rank == 0)
+      for (int i = g > ST ? g - ST : 0; i < g; ++i)
+        if (!mbar_wait(&full[i % ST], (i / ST) & 1, SITE_LINEAR)) break;
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---------------- MMA issuer (leader)
+    const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
+                           ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+    bool ok = true;
+    int g = 0, it = 0;
+    for (int t = cluster; ok && t < ntiles; t += nclusters) {
+      for (int kb = 0; ok && kb < nkb; ++kb, ++g) {
+        const bool first = MODE == LIN_GRAD ? kb % LT_CHUNK == 0 : kb == 0;
+        const bool last = kb == nkb - 1 || (MODE == LIN_GRAD && kb % LT_CHUNK == LT_CHUNK - 1);
+        const int buf = it & 1;
+        if (first && it >= 2 && !mbar_wait(&acc_empty[buf], ((it >> 1) - 1) & 1, SITE_LINEAR)) {
+          ok = false;
+          break;
+        }
+        const int s = g % ST;
+        if (!mbar_wait(&full[s], (g / ST) & 1, SITE_LINEAR)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + buf * BN;
+        const uint32_t sa = smem_u32(smem + s * L::STAGE_BYTES);
+        const uint32_t sb = sa + L::A_BYTES;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t da = AMN ? umma_desc_mn_sw128(sa + k * 2048, 8192) : umma_desc_k_sw128(sa + k * 32);
+          const uint64_t db = BMN ? umma_desc_mn_sw128(sb + k * 2048, 8192) : umma_desc_k_sw128(sb + k * 32);
+          umma_pair(acc, da, db, idesc, (!first || k > 0) ? 1u : 0u);
+        }
+        umma_commit_pair(&empty[s]);
+        if (last) {
+          umma_commit_pair(&acc_full[buf]);
+          ++it;
+        }
+      }
+    }
+  } else if (warp >= 2) {
+    // ---------------- epilogue
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stg = smem + L::STG_OFF + (warp - 2) * 2 * 4096;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
+    const uint32_t empty_leader[2] = {map_rank(smem_u32(&acc_empty[0]), 0), map_rank(smem_u32(&acc_empty[1]), 0)};
+    int nst = 0;
+    auto stage_wait = [&] {  // the store that last read staging tile nst & 1 is done
+      if (lane == 0 && nst >= 2) bulk_wait_group_read<1>();
+      __syncwarp();
+    };
+    auto stage_done = [&] {
+      if (lane == 0) bulk_commit_group();
+      ++nst;
+    };
+    int it = 0;
+    for (int t = cluster; t < ntiles; t += nclusters) {
+      int r0, c0;
+      tile_at(t, r0, c0);
+      const int rw = r0 + (int)rank * 128 + quarter * 32;  // the warp's first row
+      const int r = rw + lane;
+      const int cw = c0 + half * (BN / 2);                 // the warp's first column
+      if (MODE == LIN_OUT) {
+        const int buf = it & 1;
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (it >> 1) & 1, SITE_LINEAR));
+        if (!ok) break;
+        tc_fence_after();
+        const bool whole = rw + 32 <= rows;
+#pragma unroll 1
+        for (int cc = 0; cc < BN / 128; ++cc) {
+          const int n = cw + cc * 64;
+          uint32_t raw[64];
+          tmem_ld32_nowait(lane_base + buf * BN + cc * 64, raw);
+          tmem_ld32_nowait(lane_base + buf * BN + cc * 64 + 32, raw + 32);
+          tmem_wait_ld();
+          if (cc == BN / 128 - 1) {  // the accumulator is read: release it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_leader[buf]);
+          }
+          if (n >= p.C || rw >= rows) continue;
+          const bool full_cols = n + 64 <= p.C;
+          float v[64];
+#pragma unroll
+          for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(raw[i]);
+          if (p.bias) {
+            if (full_cols && aligned16_dev(p.bias)) {
+#pragma unroll
+              for (int i = 0; i < 64; i += 8) {
+                float b[8];
+                load_params<8>(p.bias, p.bias_bf16, n + i, 0.f, b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i + e] += b[e];
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (n + i < p.C) {
+                  float b;
+                  load_params<1>(p.bias, p.bias_bf16, n + i, 0.f, &b);
+                  v[i] += b;
+                }
+            }
+          }
+          if (p.pre) {
+            if (whole && p.pre_tma) {
+              stage_wait();
+              uint8_t* tb = stg + (nst & 1) * 4096;
+              uint32_t w[16];
+              pack32<false>(v, w);
+              stage_row32(tb, lane, 0, w);
+              pack32<false>(v + 32, w);
+              stage_row32(tb, lane, 4, w);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) tma_store_2d(&tmPre, tb, n, rw);
+              stage_done();
+            } else if (r < rows) {
+              bf16* o = p.pre + (int64_t)r * p.ldp + n;
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (n + i < p.C) o[i] = __float2bfloat16_rn(v[i]);
+            }
+          }
+          if (p.act != JENGA_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) v[i] = act_value(v[i], p.act);
+          }
+          if (p.residual && r < rows) {
+            const bf16* q = p.residual + (int64_t)r * p.ldr + n;
+            if (full_cols && (p.ldr & 7) == 0 && aligned16_dev(p.residual)) {
+#pragma unroll
+              for (int i = 0; i < 64; i += 32) {
+                float f[32];
+                load_bf16x32(q + i, f);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[i + e] += f[e];
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (n + i < p.C) v[i] += __bfloat162float(q[i]);
+            }
+          }
+          if (whole && p.out_tma) {
+            stage_wait();
+            uint8_t* tb = stg + (nst & 1) * 4096;
+            uint32_t w[16];
+            pack32<false>(v, w);
+            stage_row32(tb, lane, 0, w);
+            pack32<false>(v + 32, w);
+            stage_row32(tb, lane, 4, w);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tma_store_2d(&tmOut, tb, n, rw);
+            stage_done();
+          } else if (r < rows) {
+            bf16* o = reinterpret_cast<bf16*>(p.out) + (int64_t)r * p.ldo + n;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (n + i < p.C) o[i] = __float2bfloat16_rn(v[i]);
+          }
+        }
+        ++it;
+      } else {
+        // LIN_GRAD: add the chunks in fp32 registers, then write the tile
+        float acc[BN / 2];
+#pragma unroll
+        for (int i = 0; i < BN / 2; ++i) acc[i] = 0.f;
+        bool ok = true;
+        for (int kb = 0; kb < nkb; kb += LT_CHUNK) {
+          const int buf = it & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (it >> 1) & 1, SITE_LINEAR));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) {
+            uint32_t raw[32];
+            tmem_ld32_nowait(lane_base + buf * BN + c * 32, raw);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c * 32 + i] += __uint_as_float(raw[i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(empty_leader[buf]);
+          ++it;
+        }
+        if (!ok) break;
+        const bool whole = rw + 32 <= rows;
+#pragma unroll
+        for (int c = 0; c < BN / 64; ++c) {
+          const int n = cw + c * 32;
+          if (n >= p.C || rw >= rows) continue;
+          const float* v = acc + c * 32;
+          if (whole && p.out_tma) {
+            stage_wait();
+            uint8_t* tb = stg + (nst & 1) * 4096;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(tb + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                  make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (p.accumulate)
+                tma_reduce_add_2d(&tmOut, tb, n, rw);
+              else
+                tma_store_2d(&tmOut, tb, n, rw);
+            }
+            stage_done();
+          } else if (r < rows) {
+            float* o = reinterpret_cast<float*>(p.out) + (int64_t)r * p.ldo + n;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (n + i < p.C) o[i] = p.accumulate ? o[i] + v[i] : v[i];
+          }
+        }
+      }
+    }
+    if (lane == 0 && nst > 0) bulk_wait_group_read<0>();  // staging outlives the stores' reads
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * BN);
+  }
+}
+
+}  // namespace jenga

@@ -1,0 +1,169 @@
+// Shared pieces of the row-wise operators (layer norm, dropout, the linear layer's
+// element-wise passes): the retained-row map and 16-byte row vectors.
+#pragma once
+
+#include "common.cuh"
+
+namespace jenga {
+
+// Rows of an operator call.  Compact row r (0 <= r < rows) is sequence row r without a block
+// list and idx[r / blk] * blk + r % blk with one.  n_kept (device, nullable) counts the valid
+// blocks: rows at and past *n_kept * blk are neither read nor written.
+struct RowMap {
+  const int32_t* idx;
+  const int32_t* n_kept;
+  int blk, nb, rows;
+};
+
+// Valid rows of the call; an n_kept outside [0, rows / blk] is recorded and nothing is done.
+__device__ __forceinline__ int valid_rows(const RowMap& m) {
+  if (!m.n_kept) return m.rows;
+  const int nk = __ldg(m.n_kept);
+  if (nk < 0 || (int64_t)nk * m.blk > m.rows) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) record_device_error(JENGA_EINTERNAL, SITE_NKEPT_RANGE, (unsigned)nk);
+    return 0;
+  }
+  return nk * m.blk;
+}
+
+// Sequence row of compact row r, or -1 for a list entry that is out of range or does not
+// ascend (a block listed twice would make two rows write one place).
+__device__ __forceinline__ int64_t sequence_row(const RowMap& m, int r) {
+  if (!m.idx) return r;
+  const int i = r / m.blk;
+  const int b = __ldg(m.idx + i);
+  if (b < 0 || b >= m.nb || (i > 0 && __ldg(m.idx + i - 1) >= b)) return -1;
+  return (int64_t)b * m.blk + (r - i * m.blk);
+}
+
+// VEC consecutive elements of a row as loaded: one 16-byte vector (VEC = 16 / sizeof(T)), or
+// one element (VEC = 1) for rows that are not 16-byte aligned.
+template <typename T, int VEC>
+struct RowVec;
+template <>
+struct RowVec<bf16, 8> {
+  uint4 r;
+  __device__ __forceinline__ void load(const bf16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(bf16* p, const float* f) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7]));
+  }
+};
+template <>
+struct RowVec<float, 4> {
+  float4 r;
+  __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = r.x;
+    f[1] = r.y;
+    f[2] = r.z;
+    f[3] = r.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float* f) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+};
+template <>
+struct RowVec<bf16, 1> {
+  bf16 r;
+  __device__ __forceinline__ void load(const bf16* p) { r = *p; }
+  __device__ __forceinline__ void zero() { r = __float2bfloat16_rn(0.f); }
+  __device__ __forceinline__ void get(float* f) const { f[0] = __bfloat162float(r); }
+  static __device__ __forceinline__ void store(bf16* p, const float* f) { *p = __float2bfloat16_rn(f[0]); }
+};
+template <>
+struct RowVec<float, 1> {
+  float r;
+  __device__ __forceinline__ void load(const float* p) { r = *p; }
+  __device__ __forceinline__ void zero() { r = 0.f; }
+  __device__ __forceinline__ void get(float* f) const { f[0] = r; }
+  static __device__ __forceinline__ void store(float* p, const float* f) { *p = f[0]; }
+};
+
+// N consecutive parameters (N = 1, 4 or 8) of type F32 or BF16; `fill` without a tensor.
+// N > 1 needs a 16-byte aligned tensor and a column that is a multiple of N.
+template <int N>
+__device__ __forceinline__ void load_params(const void* p, int wbf16, int64_t col, float fill, float* f) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = fill;
+  } else if (wbf16) {
+    const bf16* q = reinterpret_cast<const bf16*>(p) + col;
+    if constexpr (N == 1) {
+      f[0] = __bfloat162float(*q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(q + i));
+        f[i] = __uint_as_float(w.x << 16);
+        f[i + 1] = __uint_as_float(w.x & 0xffff0000u);
+        f[i + 2] = __uint_as_float(w.y << 16);
+        f[i + 3] = __uint_as_float(w.y & 0xffff0000u);
+      }
+    }
+  } else {
+    const float* q = reinterpret_cast<const float*>(p) + col;
+    if constexpr (N == 1) {
+      f[0] = *q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(q + i));
+        f[i] = w.x;
+        f[i + 1] = w.y;
+        f[i + 2] = w.z;
+        f[i + 3] = w.w;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over the `n` warps (one of them this thread's) of the row group that shares named
+// barrier `bar`; `slot` holds a float per warp.  Two alternating slots need one barrier a sum:
+// a warp writes a slot again only after every warp has passed the other slot's barrier, that is
+// after every warp has read this one.
+__device__ __forceinline__ float group_sum(float v, float* slot, int warp, int n, int bar) {
+  v = warp_sum(v);
+  if (n == 1) return v;
+  if ((threadIdx.x & 31) == 0) slot[warp] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(n * 32) : "memory");
+  float s = 0.f;
+  for (int i = 0; i < n; ++i) s += slot[i];
+  return s;
+}
+
+__device__ __forceinline__ bool aligned16_dev(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// ------------------------------------------------------------------ host checks
+// Bytes of a [rows, cols] matrix with row pitch ld.
+inline uint64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int es) {
+  return rows < 1 || cols < 1 ? 0 : ((uint64_t)(rows - 1) * ld + cols) * es;
+}
+// May an output at `a` share memory with an input at `b`?  Yes when they are the same matrix
+// (one thread reads an element before it writes it) or do not meet.
+inline bool alias_ok(const void* a, int64_t lda, uint64_t na, const void* b, int64_t ldb, uint64_t nb,
+                     bool same_ok) {
+  if (!a || !b || !na || !nb) return true;
+  if (a == b && lda == ldb && same_ok) return true;
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x + na <= y || y + nb <= x;
+}
+inline bool is16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace jenga
