@@ -126,6 +126,35 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// Bounded wait like mbar_wait, reading the timer and the budget only every 256 polls (each poll
+// itself suspends for a hardware-defined time): those reads sit on the critical path otherwise.
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t phase) {
+  if (mbar_try_wait(bar, phase)) return true;
+  unsigned long long t0 = 0;
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (mbar_try_wait(bar, phase)) return true;
+    const unsigned long long t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > g_wait_budget_ns) {
+      record_device_error(JENGA_ETIMEOUT, SITE_LINEAR, phase);
+      return false;
+    }
+  }
+}
+
+// One lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // ---- activations (fp32)
 __device__ __forceinline__ float act_value(float z, int act) {
   if (act == JENGA_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
@@ -159,7 +188,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   uint64_t* acc_empty = acc_full + 2;  // [2], used in the leader
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_empty + 2);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
   // LIN_OUT: the valid rows bound the row tiles; LIN_GRAD: they are the reduction
@@ -195,10 +224,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == 0 && lane == 0) {
-    // ---------------- TMA producer
-    prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
+  if (warp == 0) {
+    // ---------------- TMA producer (the warp stays converged and elects a lane to issue: from a
+    // divergent lane each copy or MMA took about 100 clocks to issue, 700 per k-block for 530)
+    if (elect_one()) {
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmB);
+    }
     int g = 0;
     bool ok = true;
     for (int t = cluster; ok && t < ntiles; t += nclusters) {
@@ -208,40 +240,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       c0 += rank * (BN / 2);
       for (int kb = 0; kb < nkb; ++kb, ++g) {
         const int s = g % ST;
-        if (g >= ST && !mbar_wait(&empty[s], ((g / ST) - 1) & 1, SITE_LINEAR)) {
+        if (g >= ST && !__all_sync(0xffffffffu, pair_wait(&empty[s], ((g / ST) - 1) & 1))) {
           ok = false;
           break;
         }
-        uint8_t* sa = smem + s * L::STAGE_BYTES;
-        uint8_t* sb = sa + L::A_BYTES;
-        const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::STAGE_BYTES);
-        const bool lo = MODE == LIN_GRAD && kb >= nkb1;
-        const int kk = lo ? kb - nkb1 : kb;
-        const CUtensorMap* ma = lo ? &tmA2 : &tmA;
-        if (AMN) {
-          tma_load_2d_pair(sa, ma, bar, r0, kk * 64);
-          tma_load_2d_pair(sa + 8192, ma, bar, r0 + 64, kk * 64);
-        } else {
-          tma_load_2d_pair(sa, ma, bar, kk * 64, r0);
-        }
-        if (BMN) {
-          const bool tl = MODE == LIN_GRAD && p.tail && (kk + 1) * 64 > valid;
-          const CUtensorMap* mb = tl ? &tmTail : &tmB;
+        if (elect_one()) {
+          uint8_t* sa = smem + s * L::STAGE_BYTES;
+          uint8_t* sb = sa + L::A_BYTES;
+          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::STAGE_BYTES);
+          const bool lo = MODE == LIN_GRAD && kb >= nkb1;
+          const int kk = lo ? kb - nkb1 : kb;
+          const CUtensorMap* ma = lo ? &tmA2 : &tmA;
+          if (AMN) {
+            tma_load_2d_pair(sa, ma, bar, r0, kk * 64);
+            tma_load_2d_pair(sa + 8192, ma, bar, r0 + 64, kk * 64);
+          } else {
+            tma_load_2d_pair(sa, ma, bar, kk * 64, r0);
+          }
+          if (BMN) {
+            const bool tl = MODE == LIN_GRAD && p.tail && (kk + 1) * 64 > valid;
+            const CUtensorMap* mb = tl ? &tmTail : &tmB;
 #pragma unroll
-          for (int j = 0; j < BN / 128; ++j)
-            tma_load_2d_pair(sb + j * 8192, mb, bar, c0 + j * 64, tl ? 0 : kk * 64);
-        } else {
-          tma_load_2d_pair(sb, &tmB, bar, kk * 64, c0);
+            for (int j = 0; j < BN / 128; ++j)
+              tma_load_2d_pair(sb + j * 8192, mb, bar, c0 + j * 64, tl ? 0 : kk * 64);
+          } else {
+            tma_load_2d_pair(sb, &tmB, bar, kk * 64, c0);
+          }
         }
+        __syncwarp();
       }
     }
     // the pair's copies are complete before either CTA leaves (at once after a normal run: the
     // MMAs waited for the same phases)
     if (rank == 0)
       for (int i = g > ST ? g - ST : 0; i < g; ++i)
-        if (!mbar_wait(&full[i % ST], (i / ST) & 1, SITE_LINEAR)) break;
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+        if (!pair_wait(&full[i % ST], (i / ST) & 1)) break;
+  } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer (leader)
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
                            ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
@@ -252,12 +287,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         const bool first = MODE == LIN_GRAD ? kb % LT_CHUNK == 0 : kb == 0;
         const bool last = kb == nkb - 1 || (MODE == LIN_GRAD && kb % LT_CHUNK == LT_CHUNK - 1);
         const int buf = it & 1;
-        if (first && it >= 2 && !mbar_wait(&acc_empty[buf], ((it >> 1) - 1) & 1, SITE_LINEAR)) {
+        if (first && it >= 2 && !__all_sync(0xffffffffu, pair_wait(&acc_empty[buf], ((it >> 1) - 1) & 1))) {
           ok = false;
           break;
         }
         const int s = g % ST;
-        if (!mbar_wait(&full[s], (g / ST) & 1, SITE_LINEAR)) {
+        if (!__all_sync(0xffffffffu, pair_wait(&full[s], (g / ST) & 1))) {
           ok = false;
           break;
         }
@@ -265,17 +300,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         const uint32_t acc = tmem + buf * BN;
         const uint32_t sa = smem_u32(smem + s * L::STAGE_BYTES);
         const uint32_t sb = sa + L::A_BYTES;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t da = AMN ? umma_desc_mn_sw128(sa + k * 2048, 8192) : umma_desc_k_sw128(sa + k * 32);
-          const uint64_t db = BMN ? umma_desc_mn_sw128(sb + k * 2048, 8192) : umma_desc_k_sw128(sb + k * 32);
-          umma_pair(acc, da, db, idesc, (!first || k > 0) ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t da = AMN ? umma_desc_mn_sw128(sa + k * 2048, 8192) : umma_desc_k_sw128(sa + k * 32);
+            const uint64_t db = BMN ? umma_desc_mn_sw128(sb + k * 2048, 8192) : umma_desc_k_sw128(sb + k * 32);
+            umma_pair(acc, da, db, idesc, (!first || k > 0) ? 1u : 0u);
+          }
+          umma_commit_pair(&empty[s]);
+          if (last) umma_commit_pair(&acc_full[buf]);
         }
-        umma_commit_pair(&empty[s]);
-        if (last) {
-          umma_commit_pair(&acc_full[buf]);
-          ++it;
-        }
+        __syncwarp();
+        if (last) ++it;
       }
     }
   } else if (warp >= 2) {
@@ -302,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       const int cw = c0 + half * (BN / 2);                 // the warp's first column
       if (MODE == LIN_OUT) {
         const int buf = it & 1;
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (it >> 1) & 1, SITE_LINEAR));
+        const bool ok = __all_sync(0xffffffffu, pair_wait(&acc_full[buf], (it >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
         const bool whole = rw + 32 <= rows;
@@ -410,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         bool ok = true;
         for (int kb = 0; kb < nkb; kb += LT_CHUNK) {
           const int buf = it & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (it >> 1) & 1, SITE_LINEAR));
+          ok = __all_sync(0xffffffffu, pair_wait(&acc_full[buf], (it >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
