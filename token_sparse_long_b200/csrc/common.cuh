@@ -58,8 +58,9 @@ enum ErrSite : unsigned int {
   SITE_NKEPT_RANGE = 6,
   SITE_ATTN = 7,
   SITE_TEST_WAIT = 8,
-  SITE_LINEAR = 10,
   SITE_PACK_RANGE = 9,  // a weight outside fp16's range at pack time (detail: element index)
+  SITE_LINEAR = 10,
+  SITE_ROWS = 11,
 };
 
 __device__ __forceinline__ void record_device_error(unsigned code, unsigned site, unsigned detail) {

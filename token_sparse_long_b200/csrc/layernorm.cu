@@ -15,14 +15,418 @@
 
 namespace jenga {
 
-// ------------------------------------------------------------------ forward
-// One row group of `gw` warps per row, NV vectors of VEC elements per thread.  gw == 1: four
-// rows per CTA, one per warp, no block-wide step.  Wider rows: the CTA is the row group.
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__((VEC > 1 ? NV <= 4 : NV <= 16) ? 1024 : 128) layernorm_fwd_kernel(const T* x, int64_t ldx, RowMap map, int h, int gw,
+// ------------------------------------------------------------------ aligned rows
+// Rows of whole 16-byte vectors stream through a shared-memory ring: the row group's first warp
+// starts bulk copies ahead, a queue that does not depend on how many warps the registers leave
+// room for.  (An elected lane of the converged warp issues them: from a divergent lane a copy
+// takes about 100 clocks, on which the other warps wait at the next barrier; the backward of
+// 26240 x 4096 took 126 instead of 115 us.)  A group of `gw` warps -- one, or the whole CTA --
+// owns a row at a time and a thread the same NV vectors of every row; groups are persistent
+// (group g of G takes rows g, g + G, ...), so what belongs to a column stays in registers.
+// Arithmetic is on fp32 pairs.
+
+// fp32 pairs of one 16-byte vector
+template <typename T>
+__device__ __forceinline__ void vec_pairs(const uint4& r, uint64_t* f) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  } else {
+    f[0] = f2pack(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    f[1] = f2pack(__uint_as_float(w[2]), __uint_as_float(w[3]));
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pairs_vec(const uint64_t* f) {
+  uint32_t w[4];
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      f2unpack(f[i], a, b);
+      w[i] = pack_bf2(a, b);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float a, b;
+      f2unpack(f[i], a, b);
+      w[2 * i] = __float_as_uint(a);
+      w[2 * i + 1] = __float_as_uint(b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  float a, b;
+  f2unpack(v, a, b);
+  return a + b;
+}
+
+constexpr int LN_MAX_STAGES = 8;
+
+// Row group state of the ring: per stage a barrier and the sequence row (-1: a bad list
+// entry).
+struct LnRing {
+  uint64_t bar[LN_MAX_STAGES];
+  int64_t row[LN_MAX_STAGES];
+};
+
+// Arm stage s for compact row r at sequence row `row` (one lane).  False for a bad list entry, which
+// is recorded; the stage then completes at once.
+__device__ __forceinline__ bool ln_claim(LnRing& st, int64_t row, int r, int s, uint32_t bytes) {
+  st.row[s] = row;
+  if (row < 0) {
+    record_device_error(JENGA_EINTERNAL, SITE_INDEX_RANGE, (unsigned)r);
+    mbar_arrive(&st.bar[s]);
+    return false;
+  }
+  mbar_arrive_expect_tx(&st.bar[s], bytes);
+  return true;
+}
+
+// Barrier of a row group (a warp, or else the CTA) that also agrees on `ok`: a warp that timed out
+// takes all with it.
+__device__ __forceinline__ bool group_agree(bool ok, int gw) {
+  if (gw > 1) return __syncthreads_and(ok);
+  ok = __all_sync(0xffffffffu, ok);
+  __syncwarp();
+  return ok;
+}
+
+// Forward: 16 columns a thread with gamma and beta in registers; unpacked once, centred in place,
+// one barrier a row.  FULL: every thread holds NV vectors (no bounds in the loop).
+template <typename T, int NV, bool FULL, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 128 ? 6 : (MAXT <= 256 ? 3 : (MAXT <= 320 ? 2 : 1)))
+    layernorm_fwd_ring_kernel(const T* x, int64_t ldx, RowMap map, int h, int gw, int stages, const void* gamma,
+                              const void* beta, int wbf16, float eps, T* y, int64_t ldy, float* mean_out,
+                              float* rstd_out) {
+  constexpr int VEC = 16 / (int)sizeof(T), NP = VEC / 2;
+  extern __shared__ __align__(128) uint8_t s_rows[];
+  __shared__ LnRing s_ring[4];
+  __shared__ float2 s_red[2][32];  // [parity][warp]: sum, squares about the warp's mean
+  __shared__ float2 s_cnt[32];     // elements of a row that warp w of its group holds, and 1 / that
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int groups = (blockDim.x >> 5) / gw, grp = warp / gw, gwarp = warp - grp * gw;
+  const int nvec = h / VEC, step = gw * 32, t0 = gwarp * 32 + lane;
+  const int valid = valid_rows(map);
+  const int G = gridDim.x * groups, r0 = blockIdx.x * groups + grp;
+  const bool leader = t0 == 0;
+  float cnt = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) cnt += (float)(max(0, min(32, nvec - (gwarp * 32 + i * step))) * VEC);
+  const float inv_cnt = cnt > 0.f ? 1.f / cnt : 0.f, inv_h = 1.f / (float)h;
+  if (lane == 0) s_cnt[warp] = make_float2(cnt, inv_cnt);
+  const uint32_t row_bytes = (uint32_t)h * sizeof(T);
+  uint8_t* ring = s_rows + (size_t)grp * stages * row_bytes;
+  LnRing& st = s_ring[grp];
+  if (leader) {
+    for (int i = 0; i < stages; ++i) mbar_init(&st.bar[i], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  auto start = [&](int64_t r, int s) {  // first warp of the group: row r into stage s
+    if (r >= valid) return;
+    const int64_t row = sequence_row(map, (int)r);
+    if (!elect_one()) return;
+    if (!ln_claim(st, row, (int)r, s, row_bytes)) return;
+    bulk_load_1d(ring + (size_t)s * row_bytes, x + row * ldx, row_bytes, &st.bar[s]);
+  };
+  if (gwarp == 0)
+    for (int i = 0; i < stages; ++i) {
+      start(r0 + (int64_t)i * G, i);
+      __syncwarp();
+    }
+  int p2 = 1;
+  while (p2 < gw) p2 *= 2;
+  const int lw = lane & (p2 - 1);
+  const float2 other = gw > 1 && lw < gw ? s_cnt[lw] : make_float2(0.f, 0.f);
+  uint64_t ga[NV][NP], be[NV][NP];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float a[VEC], b[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) a[e] = b[e] = 0.f;
+    if (FULL || t0 + i * step < nvec) {
+      load_params<VEC>(gamma, wbf16, (int64_t)(t0 + i * step) * VEC, 1.f, a);
+      load_params<VEC>(beta, wbf16, (int64_t)(t0 + i * step) * VEC, 0.f, b);
+    }
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      ga[i][e] = f2pack(a[2 * e], a[2 * e + 1]);
+      be[i][e] = f2pack(b[2 * e], b[2 * e + 1]);
+    }
+  }
+  int it = 0, s = 0;
+  for (int64_t r = r0; r < valid; r += G, ++it) {
+    bool ok = poll_wait(&st.bar[s], (it / stages) & 1, SITE_ROWS);
+    const bool live = st.row[s] >= 0;  // the same for all threads of the group
+    const uint4* src = reinterpret_cast<const uint4*>(ring + (size_t)s * row_bytes) + t0;
+    uint64_t f[NV][NP];
+    uint64_t acc = 0;  // (0.f, 0.f)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      if (FULL || t0 + i * step < nvec) raw = src[i * step];
+      vec_pairs<T>(raw, f[i]);
+#pragma unroll
+      for (int e = 0; e < NP; ++e) acc = fadd2(acc, f[i][e]);
+    }
+    // the warp's sum and its squares about the warp's own mean: the warps then combine in one
+    // step without cancellation, sum (M2_w + n_w (mean_w - mean)^2)
+    const float sum = warp_sum(pair_sum(acc));
+    const float wm = sum * inv_cnt;
+    const uint64_t nwm = f2pack(-wm, -wm);
+    uint64_t q = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (FULL || t0 + i * step < nvec) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+          f[i][e] = fadd2(f[i][e], nwm);
+          q = ffma2(f[i][e], f[i][e], q);
+        }
+      }
+    }
+    float m2 = warp_sum(pair_sum(q)), mean = sum * inv_h;
+    if (gw > 1) {
+      if (lane == 0) s_red[it & 1][warp] = make_float2(sum, m2);
+      ok = group_agree(ok, gw);
+      // lane l takes warp l mod p2 (the next power of two): log2(p2) shuffles a sum, where a loop
+      // over the warps is a chain of shared-memory reads
+      const float2 v = lw < gw ? s_red[it & 1][lw] : make_float2(0.f, 0.f);
+      mean = v.x;
+      for (int o = p2 >> 1; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+      mean *= inv_h;
+      const float d = fmaf(v.x, other.y, -mean);
+      m2 = fmaf(other.x * d, d, v.y);
+      for (int o = p2 >> 1; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+    } else {
+      ok = group_agree(ok, gw);
+    }
+    if (!ok) return;
+    if (gwarp == 0) {  // every warp has read the row: refill its stage
+      start(r + (int64_t)stages * G, s);
+      __syncwarp();
+    }
+    if (++s == stages) s = 0;
+    if (!live) continue;
+    const float rstd = 1.f / sqrtf(m2 * inv_h + eps);
+    if (leader) {
+      if (mean_out) mean_out[r] = mean;
+      if (rstd_out) rstd_out[r] = rstd;
+    }
+    const float off = (wm - mean) * rstd;
+    const uint64_t rs = f2pack(rstd, rstd), of = f2pack(off, off);
+    uint4* yr = reinterpret_cast<uint4*>(y + r * ldy) + t0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (FULL || t0 + i * step < nvec) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) f[i][e] = ffma2(ffma2(f[i][e], rs, of), ga[i][e], be[i][e]);
+        yr[i * step] = pairs_vec<T>(f[i]);
+      }
+    }
+  }
+}
+
+// Backward: x, dy and dres rows stream through a shared-memory ring -- the group's leader starts
+// bulk copies ahead, a queue that does not depend on how many warps the registers leave room for
+// -- and a stage is refilled after the next row's barrier, when every warp has left it.  gamma
+// and the sums of dgamma and dbeta stay in registers over all the group's rows, x - mean and
+// dy gamma between the two halves of a row.  At the end the CTA's groups are added in order in
+// shared memory and the CTA's partial sums stored in ws [CTAs][2][h], which
+// layernorm_wgrad_reduce adds in order (no atomics: the same bits every run on a device).
+template <typename T, int NV, bool RES, bool FULL, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 320 ? 2 : 1)
+    layernorm_bwd_ring_kernel(const T* dy, int64_t ldy, const T* x, int64_t ldx, RowMap map, int h, int gw, int stages,
+                              const float* mean, const float* rstd, const void* gamma, int wbf16, const T* dres,
+                              int64_t ldr, T* dx, int64_t ldd, float* ws) {
+  constexpr int VEC = 16 / (int)sizeof(T), NP = VEC / 2, MATS = RES ? 3 : 2;
+  constexpr bool HOLD = MAXT != 320;  // 96 registers leave no room: x and dy are read a second time
+  extern __shared__ __align__(128) uint8_t s_rows[];
+  __shared__ LnRing s_ring[8];
+  __shared__ float2 s_red[2][32];
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int groups = (blockDim.x >> 5) / gw, grp = warp / gw, gwarp = warp - grp * gw;
+  const int nvec = h / VEC, step = gw * 32, t0 = gwarp * 32 + lane;
+  const int valid = valid_rows(map);
+  const int G = gridDim.x * groups, r0 = blockIdx.x * groups + grp;
+  const uint32_t row_bytes = (uint32_t)h * sizeof(T);
+  uint8_t* ring = s_rows + (size_t)grp * stages * MATS * row_bytes;
+  LnRing& st = s_ring[grp];
+  const bool leader = t0 == 0;
+  if (leader) {
+    for (int i = 0; i < stages; ++i) mbar_init(&st.bar[i], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  auto start = [&](int64_t r, int s) {  // first warp of the group: row r into stage s
+    if (r >= valid) return;
+    const int64_t row = sequence_row(map, (int)r);
+    if (!elect_one()) return;
+    if (!ln_claim(st, row, (int)r, s, MATS * row_bytes)) return;
+    uint8_t* d = ring + (size_t)s * MATS * row_bytes;
+    bulk_load_1d(d, x + row * ldx, row_bytes, &st.bar[s]);
+    bulk_load_1d(d + row_bytes, dy + r * ldy, row_bytes, &st.bar[s]);
+    if (RES) bulk_load_1d(d + 2 * row_bytes, dres + row * ldr, row_bytes, &st.bar[s]);
+  };
+  if (gwarp == 0)
+    for (int i = 0; i < stages; ++i) {
+      start(r0 + (int64_t)i * G, i);
+      __syncwarp();
+    }
+  uint64_t ga[NV][NP], ag[NV][NP], ab[NV][NP];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float a[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) a[e] = 0.f;
+    if (FULL || t0 + i * step < nvec) load_params<VEC>(gamma, wbf16, (int64_t)(t0 + i * step) * VEC, 1.f, a);
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      ga[i][e] = f2pack(a[2 * e], a[2 * e + 1]);
+      ag[i][e] = 0;
+      ab[i][e] = 0;
+    }
+  }
+  int p2 = 1;  // lane l adds warp l mod p2's sums
+  while (p2 < gw) p2 *= 2;
+  const int lw = lane & (p2 - 1);
+  const float inv_h = 1.f / (float)h;
+  float mu = 0.f, rs = 0.f;  // of the row to come
+  if (r0 < valid) {
+    mu = mean[r0];
+    rs = rstd[r0];
+  }
+  int it = 0, s = 0;
+  bool ok = true;
+  for (int64_t r = r0; r < valid; r += G, ++it) {
+    const float cr = rs;
+    const uint64_t nm = f2pack(-mu, -mu), r2 = f2pack(rs, rs);
+    if (r + G < valid) {
+      mu = mean[r + G];
+      rs = rstd[r + G];
+    }
+    ok = poll_wait(&st.bar[s], (it / stages) & 1, SITE_ROWS);
+    const int64_t row = st.row[s];
+    const uint8_t* d = ring + (size_t)s * MATS * row_bytes + t0 * 16;
+    float s1 = 0.f, s2 = 0.f;
+    uint64_t xc[HOLD ? NV : 1][NP], gy[HOLD ? NV : 1][NP];  // x - mean, dy gamma
+    if (row >= 0) {
+      uint64_t p1 = 0, p2 = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (FULL || t0 + i * step < nvec) {
+          uint64_t df[NP], *xi = xc[HOLD ? i : 0], *gi = gy[HOLD ? i : 0];
+          vec_pairs<T>(*reinterpret_cast<const uint4*>(d + i * step * 16), xi);
+          vec_pairs<T>(*reinterpret_cast<const uint4*>(d + row_bytes + i * step * 16), df);
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            xi[e] = fadd2(xi[e], nm);
+            gi[e] = fmul2(df[e], ga[i][e]);
+            const uint64_t n = fmul2(xi[e], r2);
+            p1 = fadd2(p1, gi[e]);
+            p2 = ffma2(gi[e], n, p2);
+            ag[i][e] = ffma2(df[e], n, ag[i][e]);
+            ab[i][e] = fadd2(ab[i][e], df[e]);
+          }
+        }
+      }
+      s1 = pair_sum(p1);
+      s2 = pair_sum(p2);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+    }
+    if (gw > 1) {
+      if (lane == 0) s_red[it & 1][warp] = make_float2(s1, s2);
+      ok = group_agree(ok, gw);
+      const float2 v = lw < gw ? s_red[it & 1][lw] : make_float2(0.f, 0.f);
+      s1 = v.x;
+      s2 = v.y;
+      for (int o = p2 >> 1; o > 0; o >>= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+      }
+    } else {
+      ok = group_agree(ok, gw);
+    }
+    if (!ok) break;
+    if (gwarp == 0 && it > 0) {
+      start(r + (int64_t)(stages - 1) * G, s ? s - 1 : stages - 1);
+      __syncwarp();
+    }
+    if (row >= 0) {
+      // dx = rstd g - rstd mean(g) - (x - mean) rstd^2 mean(g n)
+      const float c1 = -s1 * inv_h * cr, c2 = -s2 * inv_h * cr * cr;
+      const uint64_t c1p = f2pack(c1, c1), c2p = f2pack(c2, c2);
+      uint4* dst = reinterpret_cast<uint4*>(dx + row * ldd) + t0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (FULL || t0 + i * step < nvec) {
+          uint64_t o[NP], ef[NP], *xi = xc[HOLD ? i : 0], *gi = gy[HOLD ? i : 0];
+          if (!HOLD) {
+            vec_pairs<T>(*reinterpret_cast<const uint4*>(d + i * step * 16), xi);
+            vec_pairs<T>(*reinterpret_cast<const uint4*>(d + row_bytes + i * step * 16), gi);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+              xi[e] = fadd2(xi[e], nm);
+              gi[e] = fmul2(gi[e], ga[i][e]);
+            }
+          }
+          if (RES) vec_pairs<T>(*reinterpret_cast<const uint4*>(d + 2 * row_bytes + i * step * 16), ef);
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            o[e] = ffma2(gi[e], r2, ffma2(xi[e], c2p, c1p));
+            if (RES) o[e] = fadd2(o[e], ef[e]);
+          }
+          dst[i * step] = pairs_vec<T>(o);
+        }
+      }
+    }
+    if (++s == stages) s = 0;
+  }
+  if (!ws) return;
+  float* out = ws + (int64_t)blockIdx.x * 2 * h;
+  float* mine = out;
+  if (groups > 1) {  // the ring is idle once every group has left its loop
+    __syncthreads();
+    mine = reinterpret_cast<float*>(s_rows) + (int64_t)grp * 2 * h;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t)(t0 + i * step) * VEC;
+    if (FULL || t0 + i * step < nvec) {
+#pragma unroll
+      for (int e = 0; e < NP; ++e) {
+        *reinterpret_cast<uint64_t*>(mine + c + 2 * e) = ag[i][e];
+        *reinterpret_cast<uint64_t*>(mine + h + c + 2 * e) = ab[i][e];
+      }
+    }
+  }
+  if (groups == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * h; c += blockDim.x) {
+    float a = 0.f;
+    for (int g = 0; g < groups; ++g) a += reinterpret_cast<const float*>(s_rows)[(int64_t)g * 2 * h + c];
+    out[c] = a;
+  }
+}
+
+// ------------------------------------------------------------------ unaligned rows
+// The same sums with element-wise loads straight into registers, for rows that are not whole
+// 16-byte vectors (odd widths, odd pitches, unaligned bases): a thread holds NV elements, 32 gw
+// apart.  gw == 1: four rows per CTA, one per warp; wider rows: the CTA is the row group.
+template <typename T, int NV>
+__global__ void __launch_bounds__(NV <= 16 ? 1024 : 128) layernorm_fwd_kernel(const T* x, int64_t ldx, RowMap map, int h, int gw,
                                                              const void* gamma, const void* beta, int wbf16,
                                                              float eps, T* y, int64_t ldy, float* mean_out,
                                                              float* rstd_out) {
+  constexpr int VEC = 1;
   __shared__ float s_red[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gwarp = gw == 1 ? 0 : warp;
@@ -50,7 +454,7 @@ __global__ void __launch_bounds__((VEC > 1 ? NV <= 4 : NV <= 16) ? 1024 : 128) l
     for (int e = 0; e < VEC; ++e) s += f[e];
   }
   const float inv_h = 1.f / (float)h;
-  const float mean = group_sum(s, s_red[0], gwarp, gw, 1) * inv_h;
+  const float mean = group_sum(s, s_red[0], gwarp, gw) * inv_h;
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -64,7 +468,7 @@ __global__ void __launch_bounds__((VEC > 1 ? NV <= 4 : NV <= 16) ? 1024 : 128) l
       }
     }
   }
-  const float var = group_sum(q, s_red[1], gwarp, gw, 1) * inv_h;
+  const float var = group_sum(q, s_red[1], gwarp, gw) * inv_h;
   const float rstd = 1.f / sqrtf(var + eps);
   if (t0 == 0) {
     if (mean_out) mean_out[r] = mean;
@@ -86,26 +490,20 @@ __global__ void __launch_bounds__((VEC > 1 ? NV <= 4 : NV <= 16) ? 1024 : 128) l
   }
 }
 
-// ------------------------------------------------------------------ backward
-// Persistent row groups of `gw` warps (blockDim / (32 gw) groups per CTA): group g of G takes
-// rows g, g + G, ...; a thread owns the same NV * VEC columns of every row, so the sums of
-// dgamma and dbeta stay in its registers until the group's rows are done.  The CTA's groups
-// are then added in order in shared memory and the CTA's partial sums stored in ws
-// [CTAs][2][h]; layernorm_wgrad_reduce adds the CTAs in order (no atomics: the same bits every
-// run on the same device).  The next row's dy, x (and dres) are loaded before this row's two
-// sums, so the loads cover the reduction.
-template <typename T, int VEC, int NV>
+// Backward: as the ring kernel, the next row's elements loaded before this row's two sums.
+template <typename T, int NV>
 struct BwdRow {
-  RowVec<T, VEC> x[NV], dy[NV], res[NV];
+  RowVec<T, 1> x[NV], dy[NV], res[NV];
   float mean, rstd;
   int64_t row;
 };
 
-template <typename T, int VEC, int NV, bool RES, int MAXT>
+template <typename T, int NV, bool RES, int MAXT>
 __global__ void __launch_bounds__(MAXT)
     layernorm_bwd_kernel(const T* dy, int64_t ldy, const T* x, int64_t ldx, RowMap map, int h, int gw,
                          const float* mean, const float* rstd, const void* gamma, int wbf16, const T* dres,
                          int64_t ldr, T* dx, int64_t ldd, float* ws) {
+  constexpr int VEC = 1;
   extern __shared__ float s_dyn[];
   __shared__ float s_red[2][2][32];  // [parity][sum][warp of the CTA]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -124,7 +522,7 @@ __global__ void __launch_bounds__(MAXT)
     }
     if (t0 + i * step < nvec) load_params<VEC>(gamma, wbf16, (int64_t)(t0 + i * step) * VEC, 1.f, ga[i]);
   }
-  auto fetch = [&](BwdRow<T, VEC, NV>& b, int r) {
+  auto fetch = [&](BwdRow<T, NV>& b, int r) {
     b.row = -1;
     if (r >= valid) return;
     b.row = sequence_row(map, r);
@@ -147,7 +545,7 @@ __global__ void __launch_bounds__(MAXT)
     }
   };
   const float inv_h = 1.f / (float)h;
-  BwdRow<T, VEC, NV> cur, nxt;
+  BwdRow<T, NV> cur, nxt;
   const int r0 = blockIdx.x * groups + grp;
   fetch(cur, r0);
   int par = 0;
@@ -178,7 +576,7 @@ __global__ void __launch_bounds__(MAXT)
           s_red[par][0][warp] = s1;
           s_red[par][1][warp] = s2;
         }
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(gw * 32) : "memory");
+        __syncthreads();
         s1 = 0.f;
         s2 = 0.f;
         for (int i = 0; i < gw; ++i) {
@@ -246,21 +644,23 @@ __global__ void __launch_bounds__(MAXT)
 }
 
 // out[c] (+)= sum over the parts of part[p][c] for 2 h columns (dgamma, then dbeta): 32 columns
-// per CTA, eight interleaved runs of parts added in run order.
-__global__ void __launch_bounds__(256) layernorm_wgrad_reduce_kernel(const float* __restrict__ part, int parts, int h,
+// per CTA, 16 interleaved runs of parts added in run order.
+__global__ void __launch_bounds__(512) layernorm_wgrad_reduce_kernel(const float* __restrict__ part, int parts, int h,
                                                                      float* dgamma, float* dbeta, int accumulate) {
-  __shared__ float s[8][33];
+  __shared__ float s[16][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f;
-  if (c < 2 * h)
-    for (int p = run; p < parts; p += 8) a += part[(int64_t)p * 2 * h + c];
+  if (c < 2 * h) {
+#pragma unroll 8
+    for (int p = run; p < parts; p += 16) a += part[(int64_t)p * 2 * h + c];
+  }
   s[run][lane] = a;
   __syncthreads();
   if (run == 0 && c < 2 * h) {
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a += s[i][lane];
+    for (int i = 0; i < 16; ++i) a += s[i][lane];
     float* o = c < h ? dgamma : dbeta;
     if (o) {
       o += c < h ? c : c - h;
@@ -271,51 +671,184 @@ __global__ void __launch_bounds__(256) layernorm_wgrad_reduce_kernel(const float
 
 constexpr int LN_MAX_H = 16384;
 
-// CTAs of the backward: enough row groups for two CTAs an SM, at most one group per row.
-struct LnBwdShape {
-  int vec, nv, gw, groups, ctas;
+// Shape of a launch: row groups of gw warps, nv vectors (elements when vec == 1) a thread, and
+// for the ring its stages and bytes.
+struct LnShape {
+  int vec, nv, gw, groups, ctas, stages;
+  size_t smem;
 };
-static LnBwdShape ln_bwd_shape(int rows, int h, int vec) {
-  LnBwdShape s;
-  s.vec = vec;
-  const int nvec = h / vec;
-  // columns a thread owns: as few as one vector while the row group stays within 512 threads
+constexpr int LN_CTAS_PER_SM = 8;  // most of the backward (sizes the partial sums)
+
+// Aligned forward: 16 columns a thread (fewer when a warp holds the row), 24 warps an SM.
+static LnShape ln_fwd_shape(int rows, int h, int es) {
+  LnShape s{};
+  s.vec = 16 / es;
+  const int nvec = h / s.vec, most = 16 / s.vec, room = 216 * 1024;
   s.nv = 1;
-  const int most = vec == 8 ? 2 : (vec == 4 ? 4 : 16);
-  while (s.nv < most && nvec > s.nv * 512) s.nv *= 2;
+  while (s.nv < most && nvec > 32 * s.nv) s.nv *= 2;
   s.gw = (nvec + 32 * s.nv - 1) / (32 * s.nv);
-  s.groups = s.gw >= 8 ? 1 : 8 / s.gw;
-  const int want = (rows + s.groups - 1) / s.groups;
-  const int cap = 2 * sm_count();
-  s.ctas = want < 1 ? 1 : (want < cap ? want : cap);
+  s.groups = s.gw > 1 ? 1 : 4;
+  const int warps = s.gw * s.groups, per_stage = h * es * s.groups;
+  const int per_sm = warps <= 4 ? 24 / warps : (warps <= 8 ? 3 : (warps <= 10 ? 2 : 1));
+  s.stages = room / (per_stage * per_sm);  // 3 rows of 64 KB at the least
+  s.stages = s.stages > LN_MAX_STAGES ? LN_MAX_STAGES : s.stages;
+  s.smem = (size_t)s.stages * per_stage;
+  const int want = (rows + s.groups - 1) / s.groups, cap = per_sm * sm_count();
+  s.ctas = want < cap ? want : cap;
+  return s;
+}
+// Aligned backward: 16 columns a thread (gamma and the two sums stay in registers), eight warps a
+// CTA, fewer columns when a warp holds the row.  Unaligned rows, and aligned ones too wide for
+// two stages of the ring: one element a thread up to 512 threads.
+static LnShape ln_bwd_shape(int rows, int h, int es, bool aligned, int mats) {
+  LnShape s{};
+  const int room = 216 * 1024;
+  aligned = aligned && 2 * h * es * mats <= room;
+  s.vec = aligned ? 16 / es : 1;
+  const int nvec = h / s.vec, most = aligned ? 16 / s.vec : 16;
+  s.nv = 1;
+  while (s.nv < most && nvec > (aligned ? 32 : 512) * s.nv) s.nv *= 2;
+  s.gw = (nvec + 32 * s.nv - 1) / (32 * s.nv);
+  s.groups = s.gw > 1 ? 1 : 8;
+  const int warps = s.gw * s.groups, per_stage = h * es * mats * s.groups;
+  int per_sm = !aligned ? 2 : (warps > 10 ? 1 : (warps < 8 ? 16 / warps : 2));
+  if (aligned) {
+    while (per_sm > 1 && room / (per_stage * per_sm) < 3) --per_sm;  // one stage ahead while one drains
+    s.stages = room / (per_stage * per_sm);
+    s.stages = s.stages > LN_MAX_STAGES ? LN_MAX_STAGES : s.stages;
+    s.smem = (size_t)s.stages * per_stage;
+  }
+  const size_t sums = s.groups > 1 ? (size_t)s.groups * 2 * h * sizeof(float) : 0;
+  if (s.smem < sums) s.smem = sums;
+  const int want = (rows + s.groups - 1) / s.groups, cap = per_sm * sm_count();
+  s.ctas = want < cap ? want : cap;
   return s;
 }
 
-template <typename T, int VEC, int NV>
-static void ln_fwd_launch(const void* x, int64_t ldx, const RowMap& map, int h, const void* gamma, const void* beta,
-                          int wbf16, float eps, void* y, int64_t ldy, float* mean, float* rstd, cudaStream_t st) {
-  const int nvec = h / VEC, gw = (nvec + 32 * NV - 1) / (32 * NV);
-  const int threads = gw == 1 ? 128 : gw * 32;
-  const int grid = gw == 1 ? (map.rows + 3) / 4 : map.rows;
-  layernorm_fwd_kernel<T, VEC, NV><<<grid, threads, 0, st>>>((const T*)x, ldx, map, h, gw, gamma, beta, wbf16, eps,
-                                                             (T*)y, ldy, mean, rstd);
+template <typename K>
+static cudaError_t ln_smem(K kernel, size_t smem) {
+  return smem > 40 * 1024  // 48 KB without the attribute, static shared memory included
+             ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+             : cudaSuccess;
 }
 
-template <typename T, int VEC, int NV>
-static void ln_bwd_launch(const LnBwdShape& s, const void* dy, int64_t ldy, const void* x, int64_t ldx,
-                          const RowMap& map, int h, const float* mean, const float* rstd, const void* gamma,
-                          int wbf16, const void* dres, int64_t ldr, void* dx, int64_t ldd, float* ws,
-                          cudaStream_t st) {
-  const int threads = s.gw * s.groups * 32;
-  const size_t smem = s.groups > 1 && ws ? (size_t)s.groups * 2 * h * sizeof(float) : 0;
+struct LnFwdCall {
+  const void* x;
+  int64_t ldx;
+  RowMap map;
+  int h;
+  const void *gamma, *beta;
+  int wbf16;
+  float eps;
+  void* y;
+  int64_t ldy;
+  float *mean, *rstd;
+};
+template <typename T, int NV, int MAXT>
+static cudaError_t ln_fwd_ring(const LnShape& s, const LnFwdCall& c, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    kernel<<<s.ctas, threads, smem, st>>>((const T*)dy, ldy, (const T*)x, ldx, map, h, s.gw, mean, rstd, gamma, wbf16,
-                                          (const T*)dres, ldr, (T*)dx, ldd, ws);
+    if ((e = ln_smem(kernel, s.smem)) != cudaSuccess) return;
+    kernel<<<s.ctas, s.gw * s.groups * 32, s.smem, st>>>((const T*)c.x, c.ldx, c.map, c.h, s.gw, s.stages, c.gamma,
+                                                         c.beta, c.wbf16, c.eps, (T*)c.y, c.ldy, c.mean, c.rstd);
+  };
+  c.h == s.gw * 32 * s.nv * s.vec ? go(layernorm_fwd_ring_kernel<T, NV, true, MAXT>)
+                                  : go(layernorm_fwd_ring_kernel<T, NV, false, MAXT>);
+  return e;
+}
+template <typename T, int NV>
+static cudaError_t ln_fwd_one(const LnFwdCall& c, cudaStream_t st) {
+  const int gw = (c.h + 32 * NV - 1) / (32 * NV);
+  layernorm_fwd_kernel<T, NV><<<gw == 1 ? (c.map.rows + 3) / 4 : c.map.rows, gw == 1 ? 128 : gw * 32, 0, st>>>(
+      (const T*)c.x, c.ldx, c.map, c.h, gw, c.gamma, c.beta, c.wbf16, c.eps, (T*)c.y, c.ldy, c.mean, c.rstd);
+  return cudaSuccess;
+}
+template <typename T>
+static cudaError_t ln_fwd(bool aligned, const LnFwdCall& c, cudaStream_t st) {
+  if (!aligned) {
+    if (c.h <= 64) return ln_fwd_one<T, 2>(c, st);
+    if (c.h <= 256) return ln_fwd_one<T, 8>(c, st);
+    if (c.h <= 1024) return ln_fwd_one<T, 32>(c, st);
+    return ln_fwd_one<T, 16>(c, st);
+  }
+  const LnShape s = ln_fwd_shape(c.map.rows, c.h, sizeof(T));
+  constexpr int MOST = sizeof(T) == 2 ? 2 : 4;
+  if (s.nv < MOST) {  // a warp holds the row: four rows a CTA
+    if (s.nv == 1) return ln_fwd_ring<T, 1, 128>(s, c, st);
+    if constexpr (MOST == 4) return ln_fwd_ring<T, 2, 128>(s, c, st);
+  }
+  const int threads = s.gw * s.groups * 32;
+  if (threads <= 128) return ln_fwd_ring<T, MOST, 128>(s, c, st);
+  if (threads <= 256) return ln_fwd_ring<T, MOST, 256>(s, c, st);
+  if (threads <= 320) return ln_fwd_ring<T, MOST, 320>(s, c, st);
+  if (threads <= 512) return ln_fwd_ring<T, MOST, 512>(s, c, st);
+  return ln_fwd_ring<T, MOST, 1024>(s, c, st);
+}
+
+struct LnBwdCall {
+  const void* dy;
+  int64_t ldy;
+  const void* x;
+  int64_t ldx;
+  RowMap map;
+  int h;
+  const float *mean, *rstd;
+  const void* gamma;
+  int wbf16;
+  const void* dres;
+  int64_t ldr;
+  void* dx;
+  int64_t ldd;
+  float* part;
+};
+template <typename T, int NV, int MAXT>
+static cudaError_t ln_bwd_ring(const LnShape& s, const LnBwdCall& c, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto kernel) {
+    if ((e = ln_smem(kernel, s.smem)) != cudaSuccess) return;
+    kernel<<<s.ctas, s.gw * s.groups * 32, s.smem, st>>>((const T*)c.dy, c.ldy, (const T*)c.x, c.ldx, c.map, c.h, s.gw,
+                                                         s.stages, c.mean, c.rstd, c.gamma, c.wbf16, (const T*)c.dres,
+                                                         c.ldr, (T*)c.dx, c.ldd, c.part);
+  };
+  if (c.h == s.gw * 32 * s.nv * s.vec)
+    c.dres ? go(layernorm_bwd_ring_kernel<T, NV, true, true, MAXT>) : go(layernorm_bwd_ring_kernel<T, NV, false, true, MAXT>);
+  else
+    c.dres ? go(layernorm_bwd_ring_kernel<T, NV, true, false, MAXT>)
+           : go(layernorm_bwd_ring_kernel<T, NV, false, false, MAXT>);
+  return e;
+}
+template <typename T, int NV>
+static cudaError_t ln_bwd_one(const LnShape& s, const LnBwdCall& c, cudaStream_t st) {
+  const int threads = s.gw * s.groups * 32;
+  auto go = [&](auto kernel) {
+    kernel<<<s.ctas, threads, s.smem, st>>>((const T*)c.dy, c.ldy, (const T*)c.x, c.ldx, c.map, c.h, s.gw, c.mean,
+                                            c.rstd, c.gamma, c.wbf16, (const T*)c.dres, c.ldr, (T*)c.dx, c.ldd, c.part);
   };
   if (threads <= 512)
-    dres ? go(layernorm_bwd_kernel<T, VEC, NV, true, 512>) : go(layernorm_bwd_kernel<T, VEC, NV, false, 512>);
+    c.dres ? go(layernorm_bwd_kernel<T, NV, true, 512>) : go(layernorm_bwd_kernel<T, NV, false, 512>);
   else
-    dres ? go(layernorm_bwd_kernel<T, VEC, NV, true, 1024>) : go(layernorm_bwd_kernel<T, VEC, NV, false, 1024>);
+    c.dres ? go(layernorm_bwd_kernel<T, NV, true, 1024>) : go(layernorm_bwd_kernel<T, NV, false, 1024>);
+  return cudaSuccess;
+}
+template <typename T>
+static cudaError_t ln_bwd(const LnShape& s, const LnBwdCall& c, cudaStream_t st) {
+  if (s.vec == 1) {
+    if (s.nv == 1) return ln_bwd_one<T, 1>(s, c, st);
+    if (s.nv == 2) return ln_bwd_one<T, 2>(s, c, st);
+    if (s.nv == 4) return ln_bwd_one<T, 4>(s, c, st);
+    if (s.nv == 8) return ln_bwd_one<T, 8>(s, c, st);
+    return ln_bwd_one<T, 16>(s, c, st);
+  }
+  constexpr int MOST = sizeof(T) == 2 ? 2 : 4;
+  if (s.nv < MOST) {  // a warp holds the row: eight rows a CTA
+    if (s.nv == 1) return ln_bwd_ring<T, 1, 256>(s, c, st);
+    if constexpr (MOST == 4) return ln_bwd_ring<T, 2, 256>(s, c, st);
+  }
+  const int threads = s.gw * s.groups * 32;
+  if (threads <= 256) return ln_bwd_ring<T, MOST, 256>(s, c, st);
+  if (threads <= 320) return ln_bwd_ring<T, MOST, 320>(s, c, st);
+  if (threads <= 512) return ln_bwd_ring<T, MOST, 512>(s, c, st);
+  return ln_bwd_ring<T, MOST, 1024>(s, c, st);
 }
 
 // shared argument checks of the row operators
@@ -336,41 +869,6 @@ static jenga_status check_rows(const char* who, int S, int h, const int32_t* idx
 
 using namespace jenga;
 
-#define JENGA_LN_DISPATCH(FN, NVV, ...)                                   \
-  do {                                                                    \
-    if (dt == JENGA_BF16 && vec == 8) {                                   \
-      FN##_VEC(bf16, 8, NVV, __VA_ARGS__);                                \
-    } else if (dt == JENGA_F32 && vec == 4) {                             \
-      FN##_VEC(float, 4, NVV, __VA_ARGS__);                               \
-    } else if (dt == JENGA_BF16) {                                        \
-      FN##_ONE(bf16, NVV, __VA_ARGS__);                                   \
-    } else {                                                              \
-      FN##_ONE(float, NVV, __VA_ARGS__);                                  \
-    }                                                                     \
-  } while (0)
-
-#define LN_FWD_VEC(T, V, n, ...)                                    \
-  (n) == 1   ? ln_fwd_launch<T, V, 1>(__VA_ARGS__)                  \
-  : (n) == 2 ? ln_fwd_launch<T, V, 2>(__VA_ARGS__)                  \
-  : (n) == 4 ? ln_fwd_launch<T, V, 4>(__VA_ARGS__)                  \
-  : (n) == 8 ? ln_fwd_launch<T, V, 8>(__VA_ARGS__)                  \
-             : ln_fwd_launch<T, V, 16>(__VA_ARGS__)
-#define LN_FWD_ONE(T, n, ...)                                       \
-  (n) == 2    ? ln_fwd_launch<T, 1, 2>(__VA_ARGS__)                 \
-  : (n) == 8  ? ln_fwd_launch<T, 1, 8>(__VA_ARGS__)                 \
-  : (n) == 16 ? ln_fwd_launch<T, 1, 16>(__VA_ARGS__)                \
-              : ln_fwd_launch<T, 1, 32>(__VA_ARGS__)
-#define LN_BWD_VEC(T, V, n, ...)                                    \
-  (n) == 1   ? ln_bwd_launch<T, V, 1>(__VA_ARGS__)                  \
-  : (n) == 2 ? ln_bwd_launch<T, V, 2>(__VA_ARGS__)                  \
-             : ln_bwd_launch<T, V, 4>(__VA_ARGS__)
-#define LN_BWD_ONE(T, n, ...)                                       \
-  (n) == 1   ? ln_bwd_launch<T, 1, 1>(__VA_ARGS__)                  \
-  : (n) == 2 ? ln_bwd_launch<T, 1, 2>(__VA_ARGS__)                  \
-  : (n) == 4 ? ln_bwd_launch<T, 1, 4>(__VA_ARGS__)                  \
-  : (n) == 8 ? ln_bwd_launch<T, 1, 8>(__VA_ARGS__)                  \
-             : ln_bwd_launch<T, 1, 16>(__VA_ARGS__)
-
 extern "C" jenga_status jenga_layernorm_fwd(const void* x, int64_t ldx, int S, int h, const int32_t* idx,
                                             const int32_t* n_kept, int blk, int rows, const void* gamma,
                                             const void* beta, jenga_dtype wdt, float eps, jenga_dtype dt, void* y,
@@ -386,22 +884,13 @@ extern "C" jenga_status jenga_layernorm_fwd(const void* x, int64_t ldx, int S, i
   JENGA_CHECK_ARG(alias_ok(y, ldy, span_bytes(rows, h, ldy, es), x, ldx, span_bytes(S, h, ldx, es), !idx),
                   "jenga_layernorm_fwd: y overlaps x (allowed only as the same matrix, without a block list)");
   const int v = 16 / es;
-  const int vec = h % v == 0 && ldx % v == 0 && ldy % v == 0 && is16(x) && is16(y) && is16(gamma) && is16(beta) ? v : 1;
-  const RowMap map{idx, n_kept, blk, S / blk, rows};
+  const bool aligned =
+      h % v == 0 && ldx % v == 0 && ldy % v == 0 && is16(x) && is16(y) && is16(gamma) && is16(beta);
+  const LnFwdCall c{x, ldx, RowMap{idx, n_kept, blk, S / blk, rows}, h, gamma, beta, wdt == JENGA_BF16, eps, y, ldy, mean,
+                    rstd};
   cudaStream_t st = (cudaStream_t)stream;
-  const int wb = wdt == JENGA_BF16;
-  // a warp per row while the row fits its registers, else a CTA of as few warps as hold it
-  const int nvec = h / vec;
-  int nv;
-  if (vec > 1) {
-    nv = 1;
-    while (nv < 16 && nvec > 32 * nv) nv *= 2;
-    if (nvec > 32 * 16) nv = 4;
-  } else {
-    nv = nvec <= 64 ? 2 : (nvec <= 256 ? 8 : (nvec <= 1024 ? 32 : 16));
-  }
   const int _ps = prof_begin("layernorm_fwd", st);
-  JENGA_LN_DISPATCH(LN_FWD, nv, x, ldx, map, h, gamma, beta, wb, eps, y, ldy, mean, rstd, st);
+  JENGA_CUDA_TRY(dt == JENGA_BF16 ? ln_fwd<bf16>(aligned, c, st) : ln_fwd<float>(aligned, c, st));
   prof_end(_ps, st);
   JENGA_LAUNCH_CHECK();
   return JENGA_OK;
@@ -409,7 +898,7 @@ extern "C" jenga_status jenga_layernorm_fwd(const void* x, int64_t ldx, int S, i
 
 extern "C" size_t jenga_layernorm_bwd_workspace_bytes(int rows, int h) {
   if (rows < 1 || h < 1 || h > LN_MAX_H) return 0;
-  const int cap = 2 * sm_count();
+  const int cap = LN_CTAS_PER_SM * sm_count();
   return (size_t)(rows < cap ? rows : cap) * 2 * h * sizeof(float) + 256;
 }
 
@@ -443,20 +932,18 @@ extern "C" jenga_status jenga_layernorm_bwd(const void* dy, int64_t ldy, const v
     return fail(JENGA_EWORKSPACE, "jenga_layernorm_bwd: workspace %zu < %zu", ws ? ws_bytes : (size_t)0, need);
   float* part = wgrad ? (float*)(((uintptr_t)ws + 255) & ~uintptr_t(255)) : nullptr;
   const int v = 16 / es;
-  const int vec = h % v == 0 && ldx % v == 0 && ldy % v == 0 && ldd % v == 0 && (!dres || ldr % v == 0) && is16(x) &&
-                          is16(dy) && is16(dx) && is16(dres) && is16(gamma)
-                      ? v
-                      : 1;
-  const RowMap map{idx, n_kept, blk, S / blk, rows};
-  const int wb = wdt == JENGA_BF16;
-  const LnBwdShape s = ln_bwd_shape(rows, h, vec);
+  const bool aligned = h % v == 0 && ldx % v == 0 && ldy % v == 0 && ldd % v == 0 && (!dres || ldr % v == 0) &&
+                       is16(x) && is16(dy) && is16(dx) && is16(dres) && is16(gamma);
+  const LnShape s = ln_bwd_shape(rows, h, es, aligned, dres ? 3 : 2);
+  const LnBwdCall c{dy,  ldy,  x,   ldx, RowMap{idx, n_kept, blk, S / blk, rows}, h, mean, rstd, gamma, wdt == JENGA_BF16,
+                    dres, ldr, dx, ldd, part};
   int _ps = prof_begin("layernorm_bwd", st);
-  JENGA_LN_DISPATCH(LN_BWD, s.nv, s, dy, ldy, x, ldx, map, h, mean, rstd, gamma, wb, dres, ldr, dx, ldd, part, st);
+  JENGA_CUDA_TRY(dt == JENGA_BF16 ? ln_bwd<bf16>(s, c, st) : ln_bwd<float>(s, c, st));
   prof_end(_ps, st);
   JENGA_LAUNCH_CHECK();
   if (wgrad) {
     _ps = prof_begin("layernorm_wgrad_reduce", st);
-    layernorm_wgrad_reduce_kernel<<<(2 * h + 31) / 32, 256, 0, st>>>(part, s.ctas, h, dgamma, dbeta, accumulate);
+    layernorm_wgrad_reduce_kernel<<<(2 * h + 31) / 32, 512, 0, st>>>(part, s.ctas, h, dgamma, dbeta, accumulate);
     prof_end(_ps, st);
     JENGA_LAUNCH_CHECK();
   }

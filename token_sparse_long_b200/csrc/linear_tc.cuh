@@ -126,34 +126,7 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Bounded wait like mbar_wait, reading the timer and the budget only every 256 polls (each poll
-// itself suspends for a hardware-defined time): those reads sit on the critical path otherwise.
-__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t phase) {
-  if (mbar_try_wait(bar, phase)) return true;
-  unsigned long long t0 = 0;
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-      if (mbar_try_wait(bar, phase)) return true;
-    const unsigned long long t = global_timer_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > g_wait_budget_ns) {
-      record_device_error(JENGA_ETIMEOUT, SITE_LINEAR, phase);
-      return false;
-    }
-  }
-}
-
-// One lane of a converged warp (always the same one).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t phase) { return poll_wait(bar, phase, SITE_LINEAR); }
 
 // ---- activations (fp32)
 __device__ __forceinline__ float act_value(float z, int act) {

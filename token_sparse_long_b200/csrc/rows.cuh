@@ -134,21 +134,51 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the `n` warps (one of them this thread's) of the row group that shares named
-// barrier `bar`; `slot` holds a float per warp.  Two alternating slots need one barrier a sum:
-// a warp writes a slot again only after every warp has passed the other slot's barrier, that is
-// after every warp has read this one.
-__device__ __forceinline__ float group_sum(float v, float* slot, int warp, int n, int bar) {
+// Sum over the `n` warps of a row group (one warp, or else the CTA); `slot` holds a float per
+// warp.  Two alternating slots need one barrier a sum: a warp writes a slot again only after
+// every warp has passed the other slot's barrier, that is after every warp has read this one.
+// (Barrier 0 only: a barrier number in a register reserves all 16 for the CTA, and four such
+// CTAs are all that an SM then holds.)
+__device__ __forceinline__ float group_sum(float v, float* slot, int warp, int n) {
   v = warp_sum(v);
   if (n == 1) return v;
   if ((threadIdx.x & 31) == 0) slot[warp] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(n * 32) : "memory");
+  __syncthreads();
   float s = 0.f;
   for (int i = 0; i < n; ++i) s += slot[i];
   return s;
 }
 
 __device__ __forceinline__ bool aligned16_dev(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Bounded wait like mbar_wait, reading the timer and the budget only every 256 polls (each poll
+// itself suspends for a hardware-defined time): those reads would sit on the critical path.
+__device__ __forceinline__ bool poll_wait(uint64_t* bar, uint32_t phase, unsigned site) {
+  if (mbar_try_wait(bar, phase)) return true;
+  unsigned long long t0 = 0;
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (mbar_try_wait(bar, phase)) return true;
+    const unsigned long long t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > g_wait_budget_ns) {
+      record_device_error(JENGA_ETIMEOUT, site, phase);
+      return false;
+    }
+  }
+}
+
+// One lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 
 // ------------------------------------------------------------------ host checks
 // Bytes of a [rows, cols] matrix with row pitch ld.
