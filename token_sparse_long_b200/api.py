@@ -365,57 +365,69 @@ def jenga_lm_loss_segmented(hidden, w, labels, segment_tokens=4096, dhidden=None
 
 
 # ------------------------------------------------------------------ dense sub-block operators
-class _On:
-    """The device of a call's tensors (all on one) and its stream: outputs and workspaces are
-    allocated under that stream, so the caching allocator reuses them in its order."""
+# These calls are short (a few microseconds of kernel for small inputs), so the binding passes
+# plain integers and touches each tensor attribute once.
+def _begin(stream, x, *ts):
+    """The call's device guard and stream.  All tensors are on one CUDA device; outputs and
+    workspaces are allocated under the call's stream, so the caching allocator reuses them in
+    that stream's order.  Returns (guard to leave or None, raw stream)."""
+    dev = x.get_device()
+    for t in (x, *ts):
+        if t is not None and t.get_device() != dev:
+            if not t.is_cuda or dev < 0:
+                raise ValueError("jenga: tensors must be CUDA tensors (the library has no CPU path)")
+            raise ValueError(f"jenga: tensors on {t.device} and {x.device}")
+    if dev < 0:
+        raise ValueError("jenga: tensors must be CUDA tensors (the library has no CPU path)")
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError(f"jenga: stream of device {stream.device_index}, tensors on {x.device}")
+        guard = torch.cuda.stream(stream)
+        guard.__enter__()
+        return guard, stream.cuda_stream
+    guard = None
+    if torch.cuda.current_device() != dev:
+        guard = torch.cuda.device(dev)
+        guard.__enter__()
+    return guard, torch.cuda.current_stream(dev).cuda_stream
 
-    def __init__(self, stream, *ts):
-        _need_cuda(*ts)
-        self.dev = next(t for t in ts if t is not None).device
-        for t in ts:
-            if t is not None and t.device != self.dev:
-                raise ValueError(f"jenga: tensors on {t.device} and {self.dev}")
-        if stream is not None and stream.device != self.dev:
-            raise ValueError(f"jenga: stream of {stream.device}, tensors on {self.dev}")
-        self.stream = stream
 
-    def __enter__(self):
-        self.guard = torch.cuda.stream(self.stream) if self.stream is not None else torch.cuda.device(self.dev)
-        self.guard.__enter__()
-        self.s = ctypes.c_void_p((self.stream or torch.cuda.current_stream(self.dev)).cuda_stream)
-        return self
+def _end(guard):
+    if guard is not None:
+        guard.__exit__(None, None, None)
 
-    def __exit__(self, *a):
-        return self.guard.__exit__(*a)
 
-    def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.dev)
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _mat(t, name, cols=None, rows=None, dtype=None):
     """A 2-d tensor with contiguous rows; its pitch."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: a matrix with contiguous rows required, got {tuple(t.shape)} strides {t.stride()}")
-    if (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] < rows):
-        raise ValueError(f"{name}: [{'>= ' + str(rows) if rows is not None else '*'}, {cols}] required, got {tuple(t.shape)}")
+    shape, st = t.shape, t.stride()
+    if len(shape) != 2 or (st[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: a matrix with contiguous rows required, got {tuple(shape)} strides {st}")
+    if (cols is not None and shape[1] != cols) or (rows is not None and shape[0] < rows):
+        raise ValueError(f"{name}: [{'>= ' + str(rows) if rows is not None else '*'}, {cols}] required, got {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: {dtype} required, got {t.dtype}")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if shape[0] > 1:
+        if st[0] < shape[1]:
+            raise ValueError(f"{name}: rows overlap (strides {st})")
+        return st[0]
+    return max(st[0], shape[1])
 
 
 def _vec(t, name, n, dtype=None):
-    if t is None:
-        return
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name}: contiguous {dtype if dtype is not None else ''} [{n}] required, got {t.dtype} {tuple(t.shape)}")
+    if t is not None and (t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1)
+                          or (dtype is not None and t.dtype != dtype)):
+        raise ValueError(f"{name}: contiguous {dtype if dtype is not None else ''} [{n}] required, got {t.dtype} "
+                         f"{tuple(t.shape)}")
 
 
 def _rows_arg(idx, n_kept, blk, n_kept_max, rows):
     """Rows of a call: n_kept_max blocks with a block list, else `rows`."""
     for t, name in ((idx, "idx"), (n_kept, "n_kept")):
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < 1):
             raise ValueError(f"{name}: contiguous int32 required")
     if idx is None:
         return rows
@@ -431,25 +443,29 @@ def jenga_layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, idx=None, n_kept=Non
     (n_kept_max blocks of blk rows, default all of idx) -> (y [rows, h], mean, rstd fp32 [rows]).
 
     gamma, beta: [h] fp32 or bf16 (both alike), optional.  n_kept: device int32 count of valid
-    blocks; rows past it stay as they are in the outputs."""
-    with _On(stream, x, gamma, beta, idx, n_kept, out, mean, rstd) as on:
-        S, h = x.shape
+    blocks; rows past it stay as they are in the outputs.  out may be x itself without idx."""
+    guard, s = _begin(stream, x, gamma, beta, idx, n_kept, out, mean, rstd)
+    try:
         ldx = _mat(x, "x")
+        S, h = x.shape
         rows = _rows_arg(idx, n_kept, blk, n_kept_max, S)
         _vec(gamma, "gamma", h)
         _vec(beta, "beta", h)
         if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
             raise TypeError("gamma and beta differ in dtype")
         w = gamma if gamma is not None else beta
-        y = on.empty((rows, h), x.dtype) if out is None else out
-        mean = on.empty(rows, torch.float32) if mean is None else mean
-        rstd = on.empty(rows, torch.float32) if rstd is None else rstd
-        ldy = _mat(y, "out", h, rows, x.dtype)
+        dt = _dt(x)
+        y = torch.empty((rows, h), dtype=x.dtype, device=x.device) if out is None else out
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if mean is None else mean
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd is None else rstd
+        ldy = h if out is None else _mat(y, "out", h, rows, x.dtype)
         _vec(mean, "mean", rows, torch.float32)
         _vec(rstd, "rstd", rows, torch.float32)
-        check(load().jenga_layernorm_fwd(_p(x), ldx, S, h, _p(idx), _p(n_kept), int(blk), rows, _p(gamma), _p(beta),
-                                         _dt(w) if w is not None else F32, float(eps), _dt(x), _p(y), ldy, _p(mean),
-                                         _p(rstd), on.s))
+        check(load().jenga_layernorm_fwd(x.data_ptr(), ldx, S, h, _ptr(idx), _ptr(n_kept), blk, rows, _ptr(gamma),
+                                         _ptr(beta), _dt(w) if w is not None else F32, eps, dt, y.data_ptr(), ldy,
+                                         mean.data_ptr(), rstd.data_ptr(), s))
+    finally:
+        _end(guard)
     return y, mean, rstd
 
 
@@ -461,32 +477,37 @@ def jenga_layernorm_bwd(dy, x, mean, rstd, gamma=None, idx=None, n_kept=None, bl
     dres: gradient of the residual branch, added into dx (dx may be dres: in place).  With idx
     and no dx given, rows outside the list are zero.  accumulate: add into the given dgamma and
     dbeta.  weight_grads=False skips both (None unless given)."""
-    with _On(stream, dy, x, mean, rstd, gamma, idx, n_kept, dres, dx, dgamma, dbeta, ws) as on:
-        S, h = x.shape
+    guard, s = _begin(stream, x, dy, mean, rstd, gamma, idx, n_kept, dres, dx, dgamma, dbeta, ws)
+    try:
         ldx = _mat(x, "x")
+        S, h = x.shape
         rows = _rows_arg(idx, n_kept, blk, n_kept_max, S)
         ldy = _mat(dy, "dy", h, rows, x.dtype)
         _vec(gamma, "gamma", h)
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
-            _vec(t, name, rows, torch.float32)
+        _vec(mean, "mean", rows, torch.float32)
+        _vec(rstd, "rstd", rows, torch.float32)
+        dt, dev = _dt(x), x.device
         if dx is None:
-            dx = on.empty((S, h), x.dtype) if idx is None else torch.zeros(S, h, dtype=x.dtype, device=x.device)
+            dx = torch.empty((S, h), dtype=x.dtype, device=dev) if idx is None else torch.zeros_like(x)
         ldd = _mat(dx, "dx", h, S, x.dtype)
         ldr = _mat(dres, "dres", h, S, x.dtype) if dres is not None else 0
         if weight_grads:
             if accumulate and (dgamma is None or dbeta is None):
                 raise ValueError("accumulate needs dgamma and dbeta")
-            dgamma = on.empty(h, torch.float32) if dgamma is None else dgamma
-            dbeta = on.empty(h, torch.float32) if dbeta is None else dbeta
+            dgamma = torch.empty(h, dtype=torch.float32, device=dev) if dgamma is None else dgamma
+            dbeta = torch.empty(h, dtype=torch.float32, device=dev) if dbeta is None else dbeta
         _vec(dgamma, "dgamma", h, torch.float32)
         _vec(dbeta, "dbeta", h, torch.float32)
         lib = load()
         if ws is None and (dgamma is not None or dbeta is not None):
-            ws = on.empty(lib.jenga_layernorm_bwd_workspace_bytes(rows, h), torch.uint8)
-        check(lib.jenga_layernorm_bwd(_p(dy), ldy, _p(x), ldx, S, h, _p(idx), _p(n_kept), int(blk), rows, _p(mean),
-                                      _p(rstd), _p(gamma), _dt(gamma) if gamma is not None else F32, _p(dres), ldr,
-                                      _dt(x), _p(dx), ldd, _p(dgamma), _p(dbeta), 1 if accumulate else 0, _p(ws),
-                                      ws.numel() if ws is not None else 0, on.s))
+            ws = torch.empty(lib.jenga_layernorm_bwd_workspace_bytes(rows, h), dtype=torch.uint8, device=dev)
+        check(lib.jenga_layernorm_bwd(dy.data_ptr(), ldy, x.data_ptr(), ldx, S, h, _ptr(idx), _ptr(n_kept), blk, rows,
+                                      mean.data_ptr(), rstd.data_ptr(), _ptr(gamma),
+                                      _dt(gamma) if gamma is not None else F32, _ptr(dres), ldr, dt, dx.data_ptr(),
+                                      ldd, _ptr(dgamma), _ptr(dbeta), 1 if accumulate else 0, _ptr(ws),
+                                      ws.numel() if ws is not None else 0, s))
+    finally:
+        _end(guard)
     return dx, dgamma, dbeta
 
 
@@ -497,27 +518,33 @@ def jenga_linear_fwd(x, w, bias=None, act="none", residual=None, n_kept=None, bl
 
     act: "none", "relu", "gelu" (erf) or "silu".  save_pre (or a given pre) keeps x w^T + bias for
     the backward.  n_kept: device int32 count of valid blocks of blk rows; later rows of the
-    outputs stay as they are."""
+    outputs stay as they are.  out may be residual itself."""
     bf = torch.bfloat16
-    with _On(stream, x, w, bias, residual, n_kept, out, pre, ws) as on:
+    guard, s = _begin(stream, x, w, bias, residual, n_kept, out, pre, ws)
+    try:
         ldx = _mat(x, "x", dtype=bf)
         M, K = x.shape
         ldw = _mat(w, "w", K, dtype=bf)
         N = w.shape[0]
-        _rows_arg(None, n_kept, blk, None, M)
+        if n_kept is not None:
+            _rows_arg(None, n_kept, blk, None, M)
         _vec(bias, "bias", N)
         ldr = _mat(residual, "residual", N, M, bf) if residual is not None else 0
-        y = on.empty((M, N), bf) if out is None else out
-        ldy = _mat(y, "out", N, M, bf)
+        y = torch.empty((M, N), dtype=bf, device=x.device) if out is None else out
+        ldy = N if out is None else _mat(y, "out", N, M, bf)
         if pre is None and save_pre:
-            pre = on.empty((M, N), bf)
+            pre = torch.empty((M, N), dtype=bf, device=x.device)
         ldp = _mat(pre, "pre", N, M, bf) if pre is not None else 0
         lib = load()
-        if ws is None:
-            ws = on.empty(max(lib.jenga_linear_fwd_workspace_bytes(M, N, K), 1), torch.uint8)
-        check(lib.jenga_linear_fwd(_p(x), ldx, _p(w), ldw, _p(bias), _dt(bias) if bias is not None else F32,
-                                   ACTIVATIONS[act], _p(residual), ldr, M, N, K, _p(n_kept), int(blk), _p(y), ldy,
-                                   _p(pre), ldp, _p(ws), ws.numel(), on.s))
+        nws = lib.jenga_linear_fwd_workspace_bytes(M, N, K)
+        if ws is None and nws:
+            ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
+        check(lib.jenga_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(bias),
+                                   _dt(bias) if bias is not None else F32, ACTIVATIONS[act], _ptr(residual), ldr, M, N,
+                                   K, _ptr(n_kept), blk, y.data_ptr(), ldy, _ptr(pre), ldp, _ptr(ws),
+                                   ws.numel() if ws is not None else 0, s))
+    finally:
+        _end(guard)
     return y, pre
 
 
@@ -527,30 +554,36 @@ def jenga_linear_bwd(dy, x, w, act="none", pre=None, n_kept=None, blk=1, need=("
     (dx [M, K] bf16, dw [N, K] fp32, db [N] fp32), None for what `need` leaves out.
 
     accumulate: add into the given dw and db.  The residual's gradient is dy itself."""
-    bf = torch.bfloat16
-    with _On(stream, dy, x, w, pre, n_kept, dx, dw, db, ws) as on:
-        ldx, ldw = _mat(x, "x", dtype=bf), _mat(w, "w", x.shape[1], dtype=bf)
+    bf, f32 = torch.bfloat16, torch.float32
+    guard, s = _begin(stream, x, dy, w, pre, n_kept, dx, dw, db, ws)
+    try:
+        ldx = _mat(x, "x", dtype=bf)
         M, K = x.shape
+        ldw = _mat(w, "w", K, dtype=bf)
         N = w.shape[0]
         ldy = _mat(dy, "dy", N, M, bf)
-        _rows_arg(None, n_kept, blk, None, M)
+        if n_kept is not None:
+            _rows_arg(None, n_kept, blk, None, M)
         if act != "none" and pre is None:
             raise ValueError(f"the gradient of {act} needs pre")
         ldp = _mat(pre, "pre", N, M, bf) if pre is not None else 0
-        if accumulate and (("dw" in need and dw is None) or ("db" in need and db is None)):
+        want_w, want_b, dev = "dw" in need, "db" in need, x.device
+        if accumulate and ((want_w and dw is None) or (want_b and db is None)):
             raise ValueError("accumulate needs dw and db")
-        dx = (on.empty((M, K), bf) if dx is None else dx) if "dx" in need else None
-        dw = (on.empty((N, K), torch.float32) if dw is None else dw) if "dw" in need else None
-        db = (on.empty(N, torch.float32) if db is None else db) if "db" in need else None
+        dx = (torch.empty((M, K), dtype=bf, device=dev) if dx is None else dx) if "dx" in need else None
+        dw = (torch.empty((N, K), dtype=f32, device=dev) if dw is None else dw) if want_w else None
+        db = (torch.empty(N, dtype=f32, device=dev) if db is None else db) if want_b else None
         ldd = _mat(dx, "dx", K, M, bf) if dx is not None else 0
-        lddw = _mat(dw, "dw", K, N, torch.float32) if dw is not None else 0
-        _vec(db, "db", N, torch.float32)
-        lib = load()
+        lddw = _mat(dw, "dw", K, N, f32) if dw is not None else 0
+        _vec(db, "db", N, f32)
+        lib, a = load(), ACTIVATIONS[act]
         if ws is None:
-            ws = on.empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, ACTIVATIONS[act]), torch.uint8)
-        check(lib.jenga_linear_bwd(_p(dy), ldy, _p(x), ldx, _p(w), ldw, ACTIVATIONS[act], _p(pre), ldp, M, N, K,
-                                   _p(n_kept), int(blk), _p(dx), ldd, _p(dw), lddw, _p(db), 1 if accumulate else 0,
-                                   _p(ws), ws.numel(), on.s))
+            ws = torch.empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, a), dtype=torch.uint8, device=dev)
+        check(lib.jenga_linear_bwd(dy.data_ptr(), ldy, x.data_ptr(), ldx, w.data_ptr(), ldw, a, _ptr(pre), ldp, M, N, K,
+                                   _ptr(n_kept), blk, _ptr(dx), ldd, _ptr(dw), lddw, _ptr(db), 1 if accumulate else 0,
+                                   ws.data_ptr(), ws.numel(), s))
+    finally:
+        _end(guard)
     return dx, dw, db
 
 
@@ -560,19 +593,23 @@ def jenga_dropout(x, p, seed, offset=0, residual=None, idx=None, n_kept=None, bl
     The mask is a function of (seed, offset, sequence position, column) -- recomputed, never
     stored -- with positions row0 + r, or the block list's rows with idx.  The backward is the
     same call on the gradient, without the residual.  out may be x or residual (in place)."""
-    with _On(stream, x, residual, idx, n_kept, out) as on:
+    guard, s = _begin(stream, x, residual, idx, n_kept, out)
+    try:
         ldx = _mat(x, "x")
         rows, cols = x.shape
-        _rows_arg(None, n_kept, blk, None, rows)
-        if idx is not None:
-            if idx.dtype != torch.int32 or not idx.is_contiguous() or idx.numel() * blk < rows:
-                raise ValueError("idx: contiguous int32 list of every row's block required")
+        if idx is not None or n_kept is not None:
+            _rows_arg(idx, n_kept, blk, None, rows)
+            if idx is not None and idx.numel() * blk < rows:
+                raise ValueError("idx: a list of every row's block required")
+        dt = _dt(x)
         ldr = _mat(residual, "residual", cols, rows, x.dtype) if residual is not None else 0
-        y = on.empty((rows, cols), x.dtype) if out is None else out
-        ldy = _mat(y, "out", cols, rows, x.dtype)
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if out is None else out
+        ldy = cols if out is None else _mat(y, "out", cols, rows, x.dtype)
         m64 = (1 << 64) - 1
-        check(load().jenga_dropout(_p(x), ldx, _p(residual), ldr, rows, cols, _p(idx), _p(n_kept), int(blk), int(row0),
-                                   float(p), int(seed) & m64, int(offset) & m64, _dt(x), _p(y), ldy, on.s))
+        check(load().jenga_dropout(x.data_ptr(), ldx, _ptr(residual), ldr, rows, cols, _ptr(idx), _ptr(n_kept), blk,
+                                   row0, p, seed & m64, offset & m64, dt, y.data_ptr(), ldy, s))
+    finally:
+        _end(guard)
     return y
 
 

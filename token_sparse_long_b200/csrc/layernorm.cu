@@ -95,10 +95,10 @@ __device__ __forceinline__ bool group_agree(bool ok, int gw) {
   return ok;
 }
 
-// Forward: 16 columns a thread with gamma and beta in registers; unpacked once, centred in place,
-// one barrier a row.  FULL: every thread holds NV vectors (no bounds in the loop).
+// Forward: gamma and beta in registers; a row is unpacked once, centred in place, and takes one
+// barrier.  FULL: every thread holds NV vectors (no bounds in the loop).
 template <typename T, int NV, bool FULL, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 128 ? 6 : (MAXT <= 256 ? 3 : (MAXT <= 320 ? 2 : 1)))
+__global__ void __launch_bounds__(MAXT, MAXT <= 128 ? (sizeof(T) == 2 ? 4 : 6) : (MAXT <= 160 ? 3 : (MAXT <= 320 ? 2 : 1)))
     layernorm_fwd_ring_kernel(const T* x, int64_t ldx, RowMap map, int h, int gw, int stages, const void* gamma,
                               const void* beta, int wbf16, float eps, T* y, int64_t ldy, float* mean_out,
                               float* rstd_out) {
@@ -679,17 +679,21 @@ struct LnShape {
 };
 constexpr int LN_CTAS_PER_SM = 8;  // most of the backward (sizes the partial sums)
 
-// Aligned forward: 16 columns a thread (fewer when a warp holds the row), 24 warps an SM.
+// Aligned forward.  bf16 is bound by instruction issue next to memory: 32 columns a thread spread
+// the per-row steps (barrier, shuffles, copies) over more of them, at 16 warps an SM (26240 x
+// 4096: 78 us against 92 with 16 columns and 24 warps; 5120 wide: 94 against 122).  fp32 moves
+// twice the bytes a column: 16 columns, two CTAs an SM for wide rows (16384 x 4096: 83 us
+// against 93 with 32 columns, 101 with three CTAs).  Fewer columns when a warp holds the row.
 static LnShape ln_fwd_shape(int rows, int h, int es) {
   LnShape s{};
   s.vec = 16 / es;
-  const int nvec = h / s.vec, most = 16 / s.vec, room = 216 * 1024;
+  const int nvec = h / s.vec, most = 4, room = 216 * 1024;  // 32 columns of bf16, 16 of fp32
   s.nv = 1;
   while (s.nv < most && nvec > 32 * s.nv) s.nv *= 2;
   s.gw = (nvec + 32 * s.nv - 1) / (32 * s.nv);
   s.groups = s.gw > 1 ? 1 : 4;
   const int warps = s.gw * s.groups, per_stage = h * es * s.groups;
-  const int per_sm = warps <= 4 ? 24 / warps : (warps <= 8 ? 3 : (warps <= 10 ? 2 : 1));
+  int per_sm = warps <= 4 ? (es == 2 ? 16 : 24) / warps : (es == 2 && warps <= 5 ? 3 : (warps <= (es == 2 ? 8 : 10) ? 2 : 1));
   s.stages = room / (per_stage * per_sm);  // 3 rows of 64 KB at the least
   s.stages = s.stages > LN_MAX_STAGES ? LN_MAX_STAGES : s.stages;
   s.smem = (size_t)s.stages * per_stage;
@@ -772,17 +776,19 @@ static cudaError_t ln_fwd(bool aligned, const LnFwdCall& c, cudaStream_t st) {
     return ln_fwd_one<T, 16>(c, st);
   }
   const LnShape s = ln_fwd_shape(c.map.rows, c.h, sizeof(T));
-  constexpr int MOST = sizeof(T) == 2 ? 2 : 4;
-  if (s.nv < MOST) {  // a warp holds the row: four rows a CTA
-    if (s.nv == 1) return ln_fwd_ring<T, 1, 128>(s, c, st);
-    if constexpr (MOST == 4) return ln_fwd_ring<T, 2, 128>(s, c, st);
-  }
+  if (s.nv == 1) return ln_fwd_ring<T, 1, 128>(s, c, st);  // a warp holds the row: four rows a CTA
+  if (s.nv == 2) return ln_fwd_ring<T, 2, 128>(s, c, st);
   const int threads = s.gw * s.groups * 32;
-  if (threads <= 128) return ln_fwd_ring<T, MOST, 128>(s, c, st);
-  if (threads <= 256) return ln_fwd_ring<T, MOST, 256>(s, c, st);
-  if (threads <= 320) return ln_fwd_ring<T, MOST, 320>(s, c, st);
-  if (threads <= 512) return ln_fwd_ring<T, MOST, 512>(s, c, st);
-  return ln_fwd_ring<T, MOST, 1024>(s, c, st);
+  if (threads <= 128) return ln_fwd_ring<T, 4, 128>(s, c, st);
+  if constexpr (sizeof(T) == 2) {
+    if (threads <= 160) return ln_fwd_ring<T, 4, 160>(s, c, st);
+    if (threads <= 256) return ln_fwd_ring<T, 4, 256>(s, c, st);
+    return ln_fwd_ring<T, 4, 512>(s, c, st);  // 16384 columns: 16 warps
+  } else {
+    if (threads <= 320) return ln_fwd_ring<T, 4, 320>(s, c, st);
+    if (threads <= 512) return ln_fwd_ring<T, 4, 512>(s, c, st);
+    return ln_fwd_ring<T, 4, 1024>(s, c, st);
+  }
 }
 
 struct LnBwdCall {
