@@ -465,8 +465,8 @@ JENGA_API jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void* 
  *   w without dx; the two need 16-byte aligned rows as in the forward.
  *   ws: jenga_linear_bwd_workspace_bytes(M, N, K, act) bytes (dz, partial sums).
  * fp32 accumulation, promoted out of the tensor core's accumulator every 1024 rows in dw; dz
- * enters the products as bf16 (exact for NONE and RELU), as a bf16 hi + lo pair in dw for
- * GELU and SILU.  No atomics: repeated calls on one device give identical bits.
+ * enters the products as bf16 (exact for NONE and RELU), as three bf16 parts in dw for GELU
+ * and SILU.  No atomics: repeated calls on one device give identical bits.
  * Errors: EINVAL, EWORKSPACE. */
 JENGA_API size_t jenga_linear_bwd_workspace_bytes(int M, int N, int K, jenga_activation act);
 JENGA_API jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void* x, int64_t ldx, const void* w,

@@ -367,6 +367,10 @@ def jenga_lm_loss_segmented(hidden, w, labels, segment_tokens=4096, dhidden=None
 # ------------------------------------------------------------------ dense sub-block operators
 # These calls are short (a few microseconds of kernel for small inputs), so the binding passes
 # plain integers and touches each tensor attribute once.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _begin(stream, x, *ts):
     """The call's device guard and stream.  All tensors are on one CUDA device; outputs and
     workspaces are allocated under the call's stream, so the caching allocator reuses them in
@@ -389,7 +393,7 @@ def _begin(stream, x, *ts):
     if torch.cuda.current_device() != dev:
         guard = torch.cuda.device(dev)
         guard.__enter__()
-    return guard, torch.cuda.current_stream(dev).cuda_stream
+    return guard, _raw_stream(dev)
 
 
 def _end(guard):
@@ -455,9 +459,9 @@ def jenga_layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, idx=None, n_kept=Non
             raise TypeError("gamma and beta differ in dtype")
         w = gamma if gamma is not None else beta
         dt = _dt(x)
-        y = torch.empty((rows, h), dtype=x.dtype, device=x.device) if out is None else out
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if mean is None else mean
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd is None else rstd
+        y = x.new_empty((rows, h)) if out is None else out
+        mean = x.new_empty(rows, dtype=torch.float32) if mean is None else mean
+        rstd = x.new_empty(rows, dtype=torch.float32) if rstd is None else rstd
         ldy = h if out is None else _mat(y, "out", h, rows, x.dtype)
         _vec(mean, "mean", rows, torch.float32)
         _vec(rstd, "rstd", rows, torch.float32)
@@ -486,21 +490,21 @@ def jenga_layernorm_bwd(dy, x, mean, rstd, gamma=None, idx=None, n_kept=None, bl
         _vec(gamma, "gamma", h)
         _vec(mean, "mean", rows, torch.float32)
         _vec(rstd, "rstd", rows, torch.float32)
-        dt, dev = _dt(x), x.device
+        dt = _dt(x)
         if dx is None:
-            dx = torch.empty((S, h), dtype=x.dtype, device=dev) if idx is None else torch.zeros_like(x)
+            dx = x.new_empty((S, h)) if idx is None else x.new_zeros((S, h))
         ldd = _mat(dx, "dx", h, S, x.dtype)
         ldr = _mat(dres, "dres", h, S, x.dtype) if dres is not None else 0
         if weight_grads:
             if accumulate and (dgamma is None or dbeta is None):
                 raise ValueError("accumulate needs dgamma and dbeta")
-            dgamma = torch.empty(h, dtype=torch.float32, device=dev) if dgamma is None else dgamma
-            dbeta = torch.empty(h, dtype=torch.float32, device=dev) if dbeta is None else dbeta
+            dgamma = mean.new_empty(h) if dgamma is None else dgamma
+            dbeta = mean.new_empty(h) if dbeta is None else dbeta
         _vec(dgamma, "dgamma", h, torch.float32)
         _vec(dbeta, "dbeta", h, torch.float32)
         lib = load()
         if ws is None and (dgamma is not None or dbeta is not None):
-            ws = torch.empty(lib.jenga_layernorm_bwd_workspace_bytes(rows, h), dtype=torch.uint8, device=dev)
+            ws = x.new_empty(lib.jenga_layernorm_bwd_workspace_bytes(rows, h), dtype=torch.uint8)
         check(lib.jenga_layernorm_bwd(dy.data_ptr(), ldy, x.data_ptr(), ldx, S, h, _ptr(idx), _ptr(n_kept), blk, rows,
                                       mean.data_ptr(), rstd.data_ptr(), _ptr(gamma),
                                       _dt(gamma) if gamma is not None else F32, _ptr(dres), ldr, dt, dx.data_ptr(),
@@ -530,15 +534,15 @@ def jenga_linear_fwd(x, w, bias=None, act="none", residual=None, n_kept=None, bl
             _rows_arg(None, n_kept, blk, None, M)
         _vec(bias, "bias", N)
         ldr = _mat(residual, "residual", N, M, bf) if residual is not None else 0
-        y = torch.empty((M, N), dtype=bf, device=x.device) if out is None else out
+        y = x.new_empty((M, N)) if out is None else out
         ldy = N if out is None else _mat(y, "out", N, M, bf)
         if pre is None and save_pre:
-            pre = torch.empty((M, N), dtype=bf, device=x.device)
+            pre = x.new_empty((M, N))
         ldp = _mat(pre, "pre", N, M, bf) if pre is not None else 0
         lib = load()
         nws = lib.jenga_linear_fwd_workspace_bytes(M, N, K)
         if ws is None and nws:
-            ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
+            ws = x.new_empty(nws, dtype=torch.uint8)
         check(lib.jenga_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(bias),
                                    _dt(bias) if bias is not None else F32, ACTIVATIONS[act], _ptr(residual), ldr, M, N,
                                    K, _ptr(n_kept), blk, y.data_ptr(), ldy, _ptr(pre), ldp, _ptr(ws),
@@ -567,18 +571,18 @@ def jenga_linear_bwd(dy, x, w, act="none", pre=None, n_kept=None, blk=1, need=("
         if act != "none" and pre is None:
             raise ValueError(f"the gradient of {act} needs pre")
         ldp = _mat(pre, "pre", N, M, bf) if pre is not None else 0
-        want_w, want_b, dev = "dw" in need, "db" in need, x.device
+        want_w, want_b = "dw" in need, "db" in need
         if accumulate and ((want_w and dw is None) or (want_b and db is None)):
             raise ValueError("accumulate needs dw and db")
-        dx = (torch.empty((M, K), dtype=bf, device=dev) if dx is None else dx) if "dx" in need else None
-        dw = (torch.empty((N, K), dtype=f32, device=dev) if dw is None else dw) if want_w else None
-        db = (torch.empty(N, dtype=f32, device=dev) if db is None else db) if want_b else None
+        dx = (x.new_empty((M, K)) if dx is None else dx) if "dx" in need else None
+        dw = (x.new_empty((N, K), dtype=f32) if dw is None else dw) if want_w else None
+        db = (x.new_empty(N, dtype=f32) if db is None else db) if want_b else None
         ldd = _mat(dx, "dx", K, M, bf) if dx is not None else 0
         lddw = _mat(dw, "dw", K, N, f32) if dw is not None else 0
         _vec(db, "db", N, f32)
         lib, a = load(), ACTIVATIONS[act]
         if ws is None:
-            ws = torch.empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, a), dtype=torch.uint8, device=dev)
+            ws = x.new_empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, a), dtype=torch.uint8)
         check(lib.jenga_linear_bwd(dy.data_ptr(), ldy, x.data_ptr(), ldx, w.data_ptr(), ldw, a, _ptr(pre), ldp, M, N, K,
                                    _ptr(n_kept), blk, _ptr(dx), ldd, _ptr(dw), lddw, _ptr(db), 1 if accumulate else 0,
                                    ws.data_ptr(), ws.numel(), s))
@@ -603,7 +607,7 @@ def jenga_dropout(x, p, seed, offset=0, residual=None, idx=None, n_kept=None, bl
                 raise ValueError("idx: a list of every row's block required")
         dt = _dt(x)
         ldr = _mat(residual, "residual", cols, rows, x.dtype) if residual is not None else 0
-        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if out is None else out
+        y = x.new_empty((rows, cols)) if out is None else out
         ldy = cols if out is None else _mat(y, "out", cols, rows, x.dtype)
         m64 = (1 << 64) - 1
         check(load().jenga_dropout(x.data_ptr(), ldx, _ptr(residual), ldr, rows, cols, _ptr(idx), _ptr(n_kept), blk,

@@ -729,13 +729,6 @@ static LnShape ln_bwd_shape(int rows, int h, int es, bool aligned, int mats) {
   return s;
 }
 
-template <typename K>
-static cudaError_t ln_smem(K kernel, size_t smem) {
-  return smem > 40 * 1024  // 48 KB without the attribute, static shared memory included
-             ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-             : cudaSuccess;
-}
-
 struct LnFwdCall {
   const void* x;
   int64_t ldx;
@@ -752,7 +745,7 @@ template <typename T, int NV, int MAXT>
 static cudaError_t ln_fwd_ring(const LnShape& s, const LnFwdCall& c, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    if ((e = ln_smem(kernel, s.smem)) != cudaSuccess) return;
+    if ((e = allow_smem((const void*)kernel)) != cudaSuccess) return;
     kernel<<<s.ctas, s.gw * s.groups * 32, s.smem, st>>>((const T*)c.x, c.ldx, c.map, c.h, s.gw, s.stages, c.gamma,
                                                          c.beta, c.wbf16, c.eps, (T*)c.y, c.ldy, c.mean, c.rstd);
   };
@@ -811,7 +804,7 @@ template <typename T, int NV, int MAXT>
 static cudaError_t ln_bwd_ring(const LnShape& s, const LnBwdCall& c, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    if ((e = ln_smem(kernel, s.smem)) != cudaSuccess) return;
+    if ((e = allow_smem((const void*)kernel)) != cudaSuccess) return;
     kernel<<<s.ctas, s.gw * s.groups * 32, s.smem, st>>>((const T*)c.dy, c.ldy, (const T*)c.x, c.ldx, c.map, c.h, s.gw,
                                                          s.stages, c.mean, c.rstd, c.gamma, c.wbf16, (const T*)c.dres,
                                                          c.ldr, (T*)c.dx, c.ldd, c.part);

@@ -6,24 +6,26 @@
 //   dz = dy act'(pre),  dx = dz w,   dw (+)= dz^T x,   db (+)= sum_r dz
 //
 // bf16 operands, fp32 accumulation; z stays fp32 up to y's one rounding.  dz is rounded to bf16
-// to be a tensor-core operand: exact for no activation and ReLU (dy or 0).  For GELU and
-// SiLU the rounding (half a bf16 step, 2^-8 relative) is below that of the bf16 result in dx; the
-// fp32 dw takes dz as a (hi, lo) bf16 pair in two passes over the rows, which keeps 16 bits.
-// db sums dz in fp32 before any rounding.
+// to be a tensor-core operand: exact for no activation and ReLU (dy or 0).  For GELU and SiLU the
+// rounding (half a bf16 step, 2^-8 relative) is like that of the bf16 result in dx; the fp32 dw takes
+// dz as three bf16 parts (24 bits, all of dz) in three passes over the rows -- with two parts dw
+// was 4e-6 off, four times what fp32 sums lose.  db sums dz in fp32 before any rounding.
 #include "linear_tc.cuh"
 
 namespace jenga {
 
-// dz = dy act'(pre) as bf16 (hi, and lo = bf16(dz - hi)), and partial column sums of dz:
-// CTA (strip, chunk) takes 256 columns x the chunk's rows, eight columns per lane, one row per
-// warp at a time; the eight warps' sums are added in order, part[chunk][N].  Rows from the
-// valid count up to the next multiple of 64 are written as zeros (the product over the rows
-// reads whole 64-row blocks).  VEC: rows of dy and pre are 16-byte aligned.
-template <bool VEC, bool WRITE, bool LO>
+// dz = dy act'(pre) as bf16 (with PARTS = 3 also what the rounding left, twice), and partial
+// column sums of dz: CTA (strip, chunk) takes 256 columns x the chunk's rows, eight columns per
+// lane and four rows a step per warp (loads first: two matrices, one pass, bound by memory); the
+// eight warps' sums are added in order, part[chunk][N].  Rows from the valid count up to the
+// next multiple of 64 are written as zeros (the product over the rows reads whole 64-row
+// blocks).  VEC: rows of dy and pre are 16-byte aligned.
+template <bool VEC, bool WRITE, int PARTS>
 __global__ void __launch_bounds__(256)
     linear_dz_kernel(const bf16* __restrict__ dy, int64_t ldy, const bf16* __restrict__ pre, int64_t ldp, int act,
-                     int M, int N, const int32_t* n_kept, int blk, int rows_per, bf16* __restrict__ hi,
-                     bf16* __restrict__ lo, int64_t ldz, float* __restrict__ part) {
+                     int M, int N, const int32_t* n_kept, int blk, int rows_per, bf16* __restrict__ dz, int64_t ldz,
+                     int64_t part_stride, float* __restrict__ part) {
+  constexpr int STEP = 4;
   __shared__ float s_sum[8][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int valid = valid_rows(RowMap{nullptr, n_kept, blk, 0, M});
@@ -34,33 +36,38 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
   if (c < N) {
-#pragma unroll 2
-    for (int r = r_lo + warp; r < r_hi; r += 8) {
-      float d[8], z[8];
+    const bool whole = VEC && c + 8 <= N;
+    for (int r0 = r_lo + warp; r0 < r_hi; r0 += 8 * STEP) {
+      RowVec<bf16, 8> a[STEP], b[STEP];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[e] = 0.f;
-        z[e] = 0.f;
-      }
-      if (r < valid) {
-        if (VEC && c + 8 <= N) {
-          RowVec<bf16, 8> a;
-          a.load(dy + (int64_t)r * ldy + c);
-          if (act != JENGA_ACT_NONE) {
-            RowVec<bf16, 8> b;
-            b.load(pre + (int64_t)r * ldp + c);
-            b.get(z);
-          }
-          a.get(d);
-        } else {
+      for (int u = 0; u < STEP; ++u) {
+        const int r = r0 + u * 8;
+        a[u].zero();
+        b[u].zero();
+        if (r < r_hi && r < valid) {
+          if (whole) {
+            a[u].load(dy + (int64_t)r * ldy + c);
+            if (act != JENGA_ACT_NONE) b[u].load(pre + (int64_t)r * ldp + c);
+          } else {
+            bf16* av = reinterpret_cast<bf16*>(&a[u].r);
+            bf16* bv = reinterpret_cast<bf16*>(&b[u].r);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (c + e < N) {
-              d[e] = __bfloat162float(dy[(int64_t)r * ldy + c + e]);
-              if (act != JENGA_ACT_NONE) z[e] = __bfloat162float(pre[(int64_t)r * ldp + c + e]);
+            for (int e = 0; e < 8; ++e) {
+              if (c + e < N) {
+                av[e] = dy[(int64_t)r * ldy + c + e];
+                if (act != JENGA_ACT_NONE) bv[e] = pre[(int64_t)r * ldp + c + e];
+              }
             }
           }
         }
+      }
+#pragma unroll
+      for (int u = 0; u < STEP; ++u) {
+        const int r = r0 + u * 8;
+        if (r >= r_hi) break;
+        float d[8], z[8];
+        a[u].get(d);
+        b[u].get(z);
         if (act == JENGA_ACT_RELU) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) d[e] = z[e] > 0.f ? d[e] : 0.f;
@@ -70,13 +77,15 @@ __global__ void __launch_bounds__(256)
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += d[e];
-      }
-      if (WRITE) {  // the pitch is a multiple of 8: a vector may reach into the padding
-        RowVec<bf16, 8>::store(hi + (int64_t)r * ldz + c, d);
-        if (LO) {
+        if (WRITE) {  // the pitch is a multiple of 8: a vector may reach into the padding
+          bf16* o = dz + (int64_t)r * ldz + c;
+          RowVec<bf16, 8>::store(o, d);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] -= __bfloat162float(__float2bfloat16_rn(d[e]));
-          RowVec<bf16, 8>::store(lo + (int64_t)r * ldz + c, d);
+          for (int q = 1; q < PARTS; ++q) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] -= __bfloat162float(__float2bfloat16_rn(d[e]));
+            RowVec<bf16, 8>::store(o + q * part_stride, d);
+          }
         }
       }
     }
@@ -115,21 +124,112 @@ __global__ void __launch_bounds__(256) linear_tail_kernel(const bf16* __restrict
     tail[r * ldt + c] = r0 + r < valid ? x[(int64_t)(r0 + r) * ldx + c] : __float2bfloat16_rn(0.f);
 }
 
+// Forward for at most 16 rows: the weights are all the traffic, and a row tile of 256 would leave
+// most SMs without work.  x goes to shared memory as fp32; a warp takes four rows of w at a time
+// over 1 / KS of the reduction, 16-byte loads, each weight used for all MT rows of x from
+// registers (four weight rows share each read of x); KS warps' sums meet in shared memory and
+// the epilogue is the tile kernel's.  fp32 products and sums.
+constexpr int LS_R = 4;
+template <int MT>
+__global__ void __launch_bounds__(256)
+    linear_small_kernel(const bf16* __restrict__ x, int64_t ldx, const bf16* __restrict__ w, int64_t ldw, int M, int N,
+                        int K, int ks, int kchunk, const int32_t* n_kept, int blk, const void* bias, int bias_bf16,
+                        int act, const bf16* residual, int64_t ldr, bf16* y, int64_t ldy, bf16* pre, int64_t ldp) {
+  extern __shared__ __align__(16) float s_x[];  // [MT][kchunk]
+  __shared__ float s_acc[8][LS_R][MT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int valid = valid_rows(RowMap{nullptr, n_kept, blk, 0, M});
+  if (valid == 0) return;
+  const int part = warp % ks, n0 = (blockIdx.x * (8 / ks) + warp / ks) * LS_R;
+  float acc[LS_R][MT];
+#pragma unroll
+  for (int i = 0; i < LS_R; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[i][m] = 0.f;
+  for (int k0 = 0; k0 < K; k0 += kchunk) {
+    const int kn = min(kchunk, K - k0);
+    __syncthreads();  // the previous chunk is read
+    for (int i = threadIdx.x; i < MT * kchunk; i += 256) {
+      const int m = i / kchunk, k = i - m * kchunk;
+      s_x[i] = m < valid && k < kn ? __bfloat162float(x[(int64_t)m * ldx + k0 + k]) : 0.f;
+    }
+    __syncthreads();
+    if (n0 >= N) continue;
+    // rows of w are padded to 16 bytes only in pitch: the last vector of a row may be partial
+    const int nv = kn / 8, per = ks * 32;
+    const bf16* wr[LS_R];
+#pragma unroll
+    for (int i = 0; i < LS_R; ++i) wr[i] = w + (int64_t)min(n0 + i, N - 1) * ldw + k0;
+#pragma unroll 2
+    for (int v = part * 32 + lane; v < nv; v += per) {
+      RowVec<bf16, 8> wv[LS_R];
+#pragma unroll
+      for (int i = 0; i < LS_R; ++i) wv[i].load(wr[i] + v * 8);
+      float wf[LS_R][8];
+#pragma unroll
+      for (int i = 0; i < LS_R; ++i) wv[i].get(wf[i]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float4 a = *reinterpret_cast<const float4*>(s_x + m * kchunk + v * 8);
+        const float4 b = *reinterpret_cast<const float4*>(s_x + m * kchunk + v * 8 + 4);
+        const float xf[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < LS_R; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[i][m] = fmaf(wf[i][e], xf[e], acc[i][m]);
+      }
+    }
+    if (part == 0 && nv * 8 + lane < kn) {
+#pragma unroll
+      for (int i = 0; i < LS_R; ++i) {
+        const float f = __bfloat162float(wr[i][nv * 8 + lane]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[i][m] = fmaf(f, s_x[m * kchunk + nv * 8 + lane], acc[i][m]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < LS_R; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float t = warp_sum(acc[i][m]);
+      if (lane == 0) s_acc[warp][i][m] = t;
+    }
+  __syncthreads();
+  const int rows_cta = 8 / ks * LS_R;
+  for (int i = threadIdx.x; i < rows_cta * MT; i += 256) {
+    const int m = i / rows_cta, q = i - m * rows_cta;  // neighbouring threads: neighbouring columns of y
+    const int n = blockIdx.x * rows_cta + q;
+    if (n >= N || m >= valid) continue;
+    float z = 0.f;
+    for (int p = 0; p < ks; ++p) z += s_acc[q / LS_R * ks + p][q % LS_R][m];
+    if (bias) {
+      float b;
+      load_params<1>(bias, bias_bf16, n, 0.f, &b);
+      z += b;
+    }
+    if (pre) pre[(int64_t)m * ldp + n] = __float2bfloat16_rn(z);
+    z = act_value(z, act);
+    if (residual) z += __bfloat162float(residual[(int64_t)m * ldr + n]);
+    y[(int64_t)m * ldy + n] = __float2bfloat16_rn(z);
+  }
+}
+
 // ------------------------------------------------------------------ host
 struct LinMats {
-  CUtensorMap a, a2, b, tail, out, pre;
+  CUtensorMap a, a2, a3, b, tail, out, pre;
 };
 
 template <int BN, bool AMN, bool BMN, int MODE>
 static jenga_status linear_launch(const LinMats& m, const LinArgs& p, const char* name, cudaStream_t st) {
   using L = LinSmem<BN>;
   auto kernel = linear_tc_kernel<BN, AMN, BMN, MODE>;
-  JENGA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL));
+  JENGA_CUDA_TRY(allow_smem((const void*)kernel, L::TOTAL));
   const int64_t tiles = (int64_t)((p.R + 255) / 256) * ((p.C + BN - 1) / BN);
   const int pairs = sm_count() / 2;
   const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
   const int ps = prof_begin(name, st);
-  kernel<<<grid, LT_THREADS, L::TOTAL, st>>>(m.a, m.a2, m.b, m.tail, m.out, m.pre, p);
+  kernel<<<grid, LT_THREADS, L::TOTAL, st>>>(m.a, m.a2, m.a3, m.b, m.tail, m.out, m.pre, p);
   prof_end(ps, st);
   JENGA_LAUNCH_CHECK();
   return JENGA_OK;
@@ -150,19 +250,22 @@ static int dz_rows_per(int M, int N) {  // rows per chunk of linear_dz: about fo
   return per;
 }
 
+// parts that dz is held in: all of its 24 bits for dw after a smooth activation
+static int dz_parts(int act) { return act == JENGA_ACT_GELU || act == JENGA_ACT_SILU ? 3 : 1; }
+
 struct LinBwdWs {
-  bf16 *hi, *lo, *tail;
+  bf16 *dz, *tail;  // dz: `parts` matrices [M, ldz]
   float* part;
-  int64_t ldz, ldt;
+  int64_t ldz, ldt, stride;
   size_t bytes;
 };
 static LinBwdWs lin_bwd_carve(void* ws, int M, int N, int K, int act) {
   LinBwdWs w;
   w.ldz = (N + 7) / 8 * 8;
   w.ldt = (K + 7) / 8 * 8;
+  w.stride = (int64_t)M * w.ldz;
   Carve c(ws);
-  w.hi = c.take<bf16>((size_t)M * w.ldz);
-  w.lo = act == JENGA_ACT_GELU || act == JENGA_ACT_SILU ? c.take<bf16>((size_t)M * w.ldz) : nullptr;
+  w.dz = c.take<bf16>((size_t)w.stride * dz_parts(act));
   w.tail = c.take<bf16>((size_t)64 * w.ldt);
   const int per = dz_rows_per(M, N);
   w.part = c.take<float>((size_t)((M + per - 1) / per) * N);
@@ -212,6 +315,30 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
   (void)ws;
   (void)ws_bytes;
   cudaStream_t st = (cudaStream_t)stream;
+  if (M <= 16) {
+    // split the reduction inside the CTA until there are two CTAs an SM
+    int ks = 1;
+    while (ks < 8 && (int64_t)N * ks < (int64_t)8 * LS_R * 2 * sm_count() && K >= 512 * ks) ks *= 2;
+    const int rows_cta = 8 / ks * LS_R;
+    const int ps = prof_begin("linear_small", st);
+    auto go = [&](auto kernel, int mt) {
+      const int most = 96 * 1024 / 4 / mt / 8 * 8, kchunk = K < most ? (K + 7) / 8 * 8 : most;
+      const cudaError_t e = allow_smem((const void*)kernel);
+      if (e != cudaSuccess) return e;
+      kernel<<<(N + rows_cta - 1) / rows_cta, 256, (size_t)mt * kchunk * sizeof(float), st>>>(
+          (const bf16*)x, ldx, (const bf16*)w, ldw, M, N, K, ks, kchunk, n_kept, blk, bias, bias_dt == JENGA_BF16, act,
+          (const bf16*)residual, ldr, (bf16*)y, ldy, (bf16*)pre, ldp);
+      return cudaSuccess;
+    };
+    JENGA_CUDA_TRY(M == 1   ? go(linear_small_kernel<1>, 1)
+                   : M == 2 ? go(linear_small_kernel<2>, 2)
+                   : M <= 4 ? go(linear_small_kernel<4>, 4)
+                   : M <= 8 ? go(linear_small_kernel<8>, 8)
+                            : go(linear_small_kernel<16>, 16));
+    prof_end(ps, st);
+    JENGA_LAUNCH_CHECK();
+    return JENGA_OK;
+  }
   LinArgs p{};
   p.R = M;
   p.C = N;
@@ -234,7 +361,7 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
   const int64_t t256 = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
   const bool wide = t256 >= sm_count() / 2;
   JENGA_TRY(make_tmap_bf16(&m.b, w, N, K, ldw, wide ? 128 : 64));
-  m.a2 = m.tail = m.out = m.pre = m.a;
+  m.a2 = m.a3 = m.tail = m.out = m.pre = m.a;
   p.out_tma = out_map(&m.out, y, M, N, ldy);
   p.pre_tma = out_map(&m.pre, pre, M, N, ldp);
   return wide ? linear_launch<256, false, false, LIN_OUT>(m, p, "linear_fwd", st)
@@ -282,25 +409,25 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
   const LinBwdWs W = lin_bwd_carve(ws, M, N, K, act);
   // dy itself is the operand when nothing has to be computed, aligned or cut off at a device count
   const bool direct = act == JENGA_ACT_NONE && !n_kept && lin_operand_ok(dy, ldy);
-  const bf16* dz = direct ? (const bf16*)dy : W.hi;
+  const bf16* dz = direct ? (const bf16*)dy : W.dz;
   const int64_t ldz = direct ? ldy : W.ldz;
-  const bool two = W.lo && dw;
+  const int parts = dw ? dz_parts(act) : 1;
   const int per = dz_rows_per(M, N), chunks = (M + per - 1) / per;
   if (!direct || db) {
     float* part = db ? W.part : nullptr;
     const bool vec = lin_operand_ok(dy, ldy) && (!pre || lin_operand_ok(pre, ldp));
     const dim3 grid((N + 255) / 256, chunks);
     auto go = [&](auto kernel) {
-      kernel<<<grid, 256, 0, st>>>((const bf16*)dy, ldy, (const bf16*)pre, ldp, act, M, N, n_kept, blk, per, W.hi, W.lo,
-                                   W.ldz, part);
+      kernel<<<grid, 256, 0, st>>>((const bf16*)dy, ldy, (const bf16*)pre, ldp, act, M, N, n_kept, blk, per, W.dz, W.ldz,
+                                   W.stride, part);
     };
     const int ps = prof_begin("linear_dz", st);
     if (direct)
-      go(linear_dz_kernel<true, false, false>);
+      go(linear_dz_kernel<true, false, 1>);
     else if (vec)
-      two ? go(linear_dz_kernel<true, true, true>) : go(linear_dz_kernel<true, true, false>);
+      parts == 3 ? go(linear_dz_kernel<true, true, 3>) : go(linear_dz_kernel<true, true, 1>);
     else
-      two ? go(linear_dz_kernel<false, true, true>) : go(linear_dz_kernel<false, true, false>);
+      parts == 3 ? go(linear_dz_kernel<false, true, 3>) : go(linear_dz_kernel<false, true, 1>);
     prof_end(ps, st);
     JENGA_LAUNCH_CHECK();
     if (db) {
@@ -325,7 +452,7 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
     LinMats m;
     JENGA_TRY(make_tmap_bf16(&m.a, dz, M, N, ldz, 128));
     JENGA_TRY(make_tmap_bf16(&m.b, w, N, K, ldw, 64));
-    m.a2 = m.tail = m.out = m.pre = m.a;
+    m.a2 = m.a3 = m.tail = m.out = m.pre = m.a;
     p.out_tma = out_map(&m.out, dx, M, K, ldd);
     const int64_t t256 = (int64_t)((M + 255) / 256) * ((K + 255) / 256);
     JENGA_TRY((t256 >= pairs ? linear_launch<256, false, true, LIN_OUT>(m, p, "linear_dx", st)
@@ -337,7 +464,7 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
     p.C = K;
     p.m = M;
     p.nkb = (M + 63) / 64;
-    p.passes = two ? 2 : 1;
+    p.passes = parts;
     p.n_kept = n_kept;
     p.blk = blk;
     p.out = dw;
@@ -346,8 +473,11 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
     p.tail = n_kept != nullptr;
     LinMats m;
     JENGA_TRY(make_tmap_bf16(&m.a, dz, M, N, ldz, 64));
-    m.a2 = m.tail = m.out = m.pre = m.a;
-    if (two) JENGA_TRY(make_tmap_bf16(&m.a2, W.lo, M, N, W.ldz, 64));
+    m.a2 = m.a3 = m.tail = m.out = m.pre = m.a;
+    if (parts == 3) {
+      JENGA_TRY(make_tmap_bf16(&m.a2, W.dz + W.stride, M, N, W.ldz, 64));
+      JENGA_TRY(make_tmap_bf16(&m.a3, W.dz + 2 * W.stride, M, N, W.ldz, 64));
+    }
     JENGA_TRY(make_tmap_bf16(&m.b, x, M, K, ldx, 64));
     if (p.tail) {
       const int ps = prof_begin("linear_tail", st);

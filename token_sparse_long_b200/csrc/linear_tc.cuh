@@ -43,7 +43,7 @@ constexpr int LT_CHUNK = 16;
 struct LinArgs {
   int R, C, nkb;                  // rows, columns, k-blocks of one pass over the reduction
   int m;                          // host bound on the rows of x (R, or the reduction of LIN_GRAD)
-  int passes;                     // LIN_GRAD: 2 = A is a (hi, lo) pair summed over two passes
+  int passes;                     // LIN_GRAD: 3 = A is held in three parts, one pass over the rows each
   const int32_t* n_kept;          // device count of valid blocks of x's rows (nullable)
   int blk;
   const void* bias;
@@ -149,8 +149,8 @@ __device__ __forceinline__ float act_slope(float z, int act) {
 template <int BN, bool AMN, bool BMN, int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
-                     const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmTail,
-                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPre, LinArgs p) {
+                     const __grid_constant__ CUtensorMap tmA3, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmTail, const __grid_constant__ CUtensorMap tmOut,
+                     const __grid_constant__ CUtensorMap tmPre, LinArgs p) {
   using L = LinSmem<BN>;
   constexpr int ST = L::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -222,9 +222,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           uint8_t* sb = sa + L::A_BYTES;
           const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::STAGE_BYTES);
-          const bool lo = MODE == LIN_GRAD && kb >= nkb1;
-          const int kk = lo ? kb - nkb1 : kb;
-          const CUtensorMap* ma = lo ? &tmA2 : &tmA;
+          const int pass = MODE == LIN_GRAD ? (kb >= 2 * nkb1 ? 2 : (kb >= nkb1 ? 1 : 0)) : 0;
+          const int kk = kb - pass * nkb1;
+          const CUtensorMap* ma = pass == 2 ? &tmA3 : (pass == 1 ? &tmA2 : &tmA);
           if (AMN) {
             tma_load_2d_pair(sa, ma, bar, r0, kk * 64);
             tma_load_2d_pair(sa + 8192, ma, bar, r0 + 64, kk * 64);

@@ -2,6 +2,8 @@
 // element-wise passes): the retained-row map and 16-byte row vectors.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace jenga {
@@ -194,6 +196,27 @@ inline bool alias_ok(const void* a, int64_t lda, uint64_t na, const void* b, int
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x + na <= y || y + nb <= x;
 }
+// Allow a kernel `most` bytes of dynamic shared memory on the current device (set once per kernel,
+// always with the same value, and device: the call costs as much as a tenth of a short launch).
+inline cudaError_t allow_smem(const void* kernel, int most = 222 * 1024) {
+  static std::atomic<const void*> seen[16][256];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 16)
+    for (auto& slot : seen[dev]) {
+      const void* k = slot.load(std::memory_order_acquire);
+      if (k == kernel) return cudaSuccess;
+      if (!k) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        const void* none = nullptr;
+        if (e == cudaSuccess) slot.compare_exchange_strong(none, kernel);  // losing a race only sets it again later
+        return e;
+      }
+    }
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 inline bool is16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace jenga
