@@ -124,108 +124,17 @@ __global__ void __launch_bounds__(256) linear_tail_kernel(const bf16* __restrict
     tail[r * ldt + c] = r0 + r < valid ? x[(int64_t)(r0 + r) * ldx + c] : __float2bfloat16_rn(0.f);
 }
 
-// Forward for at most 16 rows: the weights are all the traffic, and a row tile of 256 would leave
-// most SMs without work.  x goes to shared memory as fp32; a warp takes four rows of w at a time
-// over 1 / KS of the reduction, 16-byte loads, each weight used for all MT rows of x from
-// registers (four weight rows share each read of x); KS warps' sums meet in shared memory and
-// the epilogue is the tile kernel's.  fp32 products and sums.
-constexpr int LS_R = 4;
-template <int MT>
-__global__ void __launch_bounds__(256)
-    linear_small_kernel(const bf16* __restrict__ x, int64_t ldx, const bf16* __restrict__ w, int64_t ldw, int M, int N,
-                        int K, int ks, int kchunk, const int32_t* n_kept, int blk, const void* bias, int bias_bf16,
-                        int act, const bf16* residual, int64_t ldr, bf16* y, int64_t ldy, bf16* pre, int64_t ldp) {
-  extern __shared__ __align__(16) float s_x[];  // [MT][kchunk]
-  __shared__ float s_acc[8][LS_R][MT];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int valid = valid_rows(RowMap{nullptr, n_kept, blk, 0, M});
-  if (valid == 0) return;
-  const int part = warp % ks, n0 = (blockIdx.x * (8 / ks) + warp / ks) * LS_R;
-  float acc[LS_R][MT];
-#pragma unroll
-  for (int i = 0; i < LS_R; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[i][m] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += kchunk) {
-    const int kn = min(kchunk, K - k0);
-    __syncthreads();  // the previous chunk is read
-    for (int i = threadIdx.x; i < MT * kchunk; i += 256) {
-      const int m = i / kchunk, k = i - m * kchunk;
-      s_x[i] = m < valid && k < kn ? __bfloat162float(x[(int64_t)m * ldx + k0 + k]) : 0.f;
-    }
-    __syncthreads();
-    if (n0 >= N) continue;
-    // rows of w are padded to 16 bytes only in pitch: the last vector of a row may be partial
-    const int nv = kn / 8, per = ks * 32;
-    const bf16* wr[LS_R];
-#pragma unroll
-    for (int i = 0; i < LS_R; ++i) wr[i] = w + (int64_t)min(n0 + i, N - 1) * ldw + k0;
-#pragma unroll 2
-    for (int v = part * 32 + lane; v < nv; v += per) {
-      RowVec<bf16, 8> wv[LS_R];
-#pragma unroll
-      for (int i = 0; i < LS_R; ++i) wv[i].load(wr[i] + v * 8);
-      float wf[LS_R][8];
-#pragma unroll
-      for (int i = 0; i < LS_R; ++i) wv[i].get(wf[i]);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const float4 a = *reinterpret_cast<const float4*>(s_x + m * kchunk + v * 8);
-        const float4 b = *reinterpret_cast<const float4*>(s_x + m * kchunk + v * 8 + 4);
-        const float xf[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < LS_R; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[i][m] = fmaf(wf[i][e], xf[e], acc[i][m]);
-      }
-    }
-    if (part == 0 && nv * 8 + lane < kn) {
-#pragma unroll
-      for (int i = 0; i < LS_R; ++i) {
-        const float f = __bfloat162float(wr[i][nv * 8 + lane]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[i][m] = fmaf(f, s_x[m * kchunk + nv * 8 + lane], acc[i][m]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < LS_R; ++i)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const float t = warp_sum(acc[i][m]);
-      if (lane == 0) s_acc[warp][i][m] = t;
-    }
-  __syncthreads();
-  const int rows_cta = 8 / ks * LS_R;
-  for (int i = threadIdx.x; i < rows_cta * MT; i += 256) {
-    const int m = i / rows_cta, q = i - m * rows_cta;  // neighbouring threads: neighbouring columns of y
-    const int n = blockIdx.x * rows_cta + q;
-    if (n >= N || m >= valid) continue;
-    float z = 0.f;
-    for (int p = 0; p < ks; ++p) z += s_acc[q / LS_R * ks + p][q % LS_R][m];
-    if (bias) {
-      float b;
-      load_params<1>(bias, bias_bf16, n, 0.f, &b);
-      z += b;
-    }
-    if (pre) pre[(int64_t)m * ldp + n] = __float2bfloat16_rn(z);
-    z = act_value(z, act);
-    if (residual) z += __bfloat162float(residual[(int64_t)m * ldr + n]);
-    y[(int64_t)m * ldy + n] = __float2bfloat16_rn(z);
-  }
-}
-
 // ------------------------------------------------------------------ host
 struct LinMats {
   CUtensorMap a, a2, a3, b, tail, out, pre;
 };
 
-template <int BN, bool AMN, bool BMN, int MODE>
+template <int BN, bool AMN, bool BMN, int MODE, bool SWAP>
 static jenga_status linear_launch(const LinMats& m, const LinArgs& p, const char* name, cudaStream_t st) {
-  using L = LinSmem<BN>;
-  auto kernel = linear_tc_kernel<BN, AMN, BMN, MODE>;
+  using L = LinSmem<BN, SWAP>;
+  auto kernel = linear_tc_kernel<BN, AMN, BMN, MODE, SWAP>;
   JENGA_CUDA_TRY(allow_smem((const void*)kernel, L::TOTAL));
-  const int64_t tiles = (int64_t)((p.R + 255) / 256) * ((p.C + BN - 1) / BN);
+  const int64_t tiles = (int64_t)((p.R + 255) / 256) * ((p.C + BN - 1) / BN) * (MODE == LIN_OUT ? p.ksplit : 1);
   const int pairs = sm_count() / 2;
   const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
   const int ps = prof_begin(name, st);
@@ -238,6 +147,85 @@ static jenga_status linear_launch(const LinMats& m, const LinArgs& p, const char
 // bf16 tensor map for an output of 32-row tiles; false when the matrix is not 16-byte aligned
 static bool out_map(CUtensorMap* map, const void* base, int rows, int cols, int64_t ld) {
   return base && is16(base) && ld % 8 == 0 && make_tmap_bf16(map, base, rows, cols, ld, 32) == JENGA_OK;
+}
+
+// Shape of a forward or dx product [M, N] over `red`: operands swapped (and the narrow side's
+// tile), tile width, ranges of the reduction.  Costs in k-blocks of a 256-wide tile (530 clocks;
+// a 128-wide one takes 390: the issue of its four MMAs and the loads do not halve), `fill` for
+// a tile's first loads and its epilogue; a split adds the pass over the partial products.
+struct LinShape {
+  bool swap;
+  int bn, ksplit;
+};
+static LinShape lin_shape(int M, int N, int red) {
+  const int pairs = sm_count() / 2, nkb = (red + 63) / 64;
+  LinShape best{};
+  double cost = 1e300;
+  auto consider = [&](bool swap, int bn) {
+    const int64_t tiles = (int64_t)(((swap ? N : M) + 255) / 256) * (((swap ? M : N) + bn - 1) / bn);
+    const double per = swap ? (bn >= 128 ? 0.75 : 0.55) : (bn >= 256 ? 1.0 : 0.75), fill = 4.0;
+    for (int s = 1; s <= 16 && s <= 1 + nkb / 8; ++s) {
+      const double waves = (double)((tiles * s + pairs - 1) / pairs);
+      double c = waves * (per * ((nkb + s - 1) / s) + fill);
+      if (s > 1) c += 10.0 + (double)s * M * N * 8.0 / 2.0e6;  // a launch; 2 MB a k-block of time through L2
+      if (c < cost * 0.97) {
+        cost = c;
+        best = LinShape{swap, bn, s};
+      }
+    }
+  };
+  if (M > 128 || N <= 128) {
+    consider(false, 256);
+    consider(false, 128);
+  } else {
+    consider(true, M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+  }
+  return best;
+}
+static size_t lin_part_bytes(const LinShape& s, int M, int N) {
+  return s.ksplit > 1 ? (size_t)s.ksplit * M * N * sizeof(float) + 256 : 0;
+}
+
+// forward or dx: x side [M, red] (K-major), weight side [N, red] K-major or (WMN) [red, N]
+template <bool WMN>
+static jenga_status lin_out(const LinShape& s, const void* x, int64_t ldx, const void* w, int64_t ldw, int M, int N,
+                            int red, LinArgs p, void* part, const char* name, cudaStream_t st) {
+  LinMats m;
+  p.m = M;
+  p.nkb = (red + 63) / 64;
+  p.passes = 1;
+  p.ksplit = s.ksplit;
+  p.part = (float*)(((uintptr_t)part + 255) & ~uintptr_t(255));
+  const int wr = WMN ? red : N, wc = WMN ? N : red;  // the weight matrix in memory
+  if (s.swap) {
+    p.R = N;
+    p.C = M;
+    JENGA_TRY(make_tmap_bf16(&m.a, w, wr, wc, ldw, WMN ? 64 : 128));
+    JENGA_TRY(make_tmap_bf16(&m.b, x, M, red, ldx, s.bn / 2));
+    m.a2 = m.a3 = m.tail = m.out = m.pre = m.a;
+    JENGA_TRY((s.bn == 32   ? linear_launch<32, WMN, false, LIN_OUT, true>(m, p, name, st)
+               : s.bn == 64 ? linear_launch<64, WMN, false, LIN_OUT, true>(m, p, name, st)
+                            : linear_launch<128, WMN, false, LIN_OUT, true>(m, p, name, st)));
+  } else {
+    p.R = M;
+    p.C = N;
+    JENGA_TRY(make_tmap_bf16(&m.a, x, M, red, ldx, 128));
+    JENGA_TRY(make_tmap_bf16(&m.b, w, wr, wc, ldw, WMN ? 64 : s.bn / 2));
+    m.a2 = m.a3 = m.tail = m.out = m.pre = m.a;
+    if (s.ksplit == 1) {
+      p.out_tma = out_map(&m.out, p.out, M, N, p.ldo);
+      p.pre_tma = out_map(&m.pre, p.pre, M, N, p.ldp);
+    }
+    JENGA_TRY((s.bn == 256 ? linear_launch<256, false, WMN, LIN_OUT, false>(m, p, name, st)
+                           : linear_launch<128, false, WMN, LIN_OUT, false>(m, p, name, st)));
+  }
+  if (s.ksplit > 1) {
+    const int ps = prof_begin("linear_finish", st);
+    linear_finish_kernel<<<dim3((N + 255) / 256, M), 256, 0, st>>>(p, N);
+    prof_end(ps, st);
+    JENGA_LAUNCH_CHECK();
+  }
+  return JENGA_OK;
 }
 
 static bool lin_operand_ok(const void* p, int64_t ld) { return is16(p) && ld % 8 == 0; }
@@ -255,7 +243,7 @@ static int dz_parts(int act) { return act == JENGA_ACT_GELU || act == JENGA_ACT_
 
 struct LinBwdWs {
   bf16 *dz, *tail;  // dz: `parts` matrices [M, ldz]
-  float* part;
+  float *part, *dxpart;
   int64_t ldz, ldt, stride;
   size_t bytes;
 };
@@ -269,6 +257,7 @@ static LinBwdWs lin_bwd_carve(void* ws, int M, int N, int K, int act) {
   w.tail = c.take<bf16>((size_t)64 * w.ldt);
   const int per = dz_rows_per(M, N);
   w.part = c.take<float>((size_t)((M + per - 1) / per) * N);
+  w.dxpart = c.take<float>((lin_part_bytes(lin_shape(M, K, N), M, K) + 3) / 4);
   w.bytes = c.used();
   return w;
 }
@@ -287,10 +276,8 @@ static jenga_status lin_check(const char* who, int M, int N, int K, const int32_
 using namespace jenga;
 
 extern "C" size_t jenga_linear_fwd_workspace_bytes(int M, int N, int K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
+  if (M < 1 || N < 1 || K < 1) return 0;
+  return lin_part_bytes(lin_shape(M, N, K), M, N);
 }
 
 extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
@@ -312,39 +299,11 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
                       alias_ok(pre, ldp, np, x, ldx, nx, false) && alias_ok(pre, ldp, np, w, ldw, nw, false) &&
                       alias_ok(pre, ldp, np, residual, ldr, nr, false),
                   "jenga_linear_fwd: an output overlaps an input (only y = residual, the same matrix, is allowed)");
-  (void)ws;
-  (void)ws_bytes;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (M <= 16) {
-    // split the reduction inside the CTA until there are two CTAs an SM
-    int ks = 1;
-    while (ks < 8 && (int64_t)N * ks < (int64_t)8 * LS_R * 2 * sm_count() && K >= 512 * ks) ks *= 2;
-    const int rows_cta = 8 / ks * LS_R;
-    const int ps = prof_begin("linear_small", st);
-    auto go = [&](auto kernel, int mt) {
-      const int most = 96 * 1024 / 4 / mt / 8 * 8, kchunk = K < most ? (K + 7) / 8 * 8 : most;
-      const cudaError_t e = allow_smem((const void*)kernel);
-      if (e != cudaSuccess) return e;
-      kernel<<<(N + rows_cta - 1) / rows_cta, 256, (size_t)mt * kchunk * sizeof(float), st>>>(
-          (const bf16*)x, ldx, (const bf16*)w, ldw, M, N, K, ks, kchunk, n_kept, blk, bias, bias_dt == JENGA_BF16, act,
-          (const bf16*)residual, ldr, (bf16*)y, ldy, (bf16*)pre, ldp);
-      return cudaSuccess;
-    };
-    JENGA_CUDA_TRY(M == 1   ? go(linear_small_kernel<1>, 1)
-                   : M == 2 ? go(linear_small_kernel<2>, 2)
-                   : M <= 4 ? go(linear_small_kernel<4>, 4)
-                   : M <= 8 ? go(linear_small_kernel<8>, 8)
-                            : go(linear_small_kernel<16>, 16));
-    prof_end(ps, st);
-    JENGA_LAUNCH_CHECK();
-    return JENGA_OK;
-  }
+  const LinShape shape = lin_shape(M, N, K);
+  const size_t need = lin_part_bytes(shape, M, N);
+  if (need && (!ws || ws_bytes < need))
+    return fail(JENGA_EWORKSPACE, "jenga_linear_fwd: workspace %zu < %zu", ws ? ws_bytes : (size_t)0, need);
   LinArgs p{};
-  p.R = M;
-  p.C = N;
-  p.m = M;
-  p.nkb = (K + 63) / 64;
-  p.passes = 1;
   p.n_kept = n_kept;
   p.blk = blk;
   p.bias = bias;
@@ -356,16 +315,7 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
   p.ldo = ldy;
   p.pre = (bf16*)pre;
   p.ldp = ldp;
-  LinMats m;
-  JENGA_TRY(make_tmap_bf16(&m.a, x, M, K, ldx, 128));
-  const int64_t t256 = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
-  const bool wide = t256 >= sm_count() / 2;
-  JENGA_TRY(make_tmap_bf16(&m.b, w, N, K, ldw, wide ? 128 : 64));
-  m.a2 = m.a3 = m.tail = m.out = m.pre = m.a;
-  p.out_tma = out_map(&m.out, y, M, N, ldy);
-  p.pre_tma = out_map(&m.pre, pre, M, N, ldp);
-  return wide ? linear_launch<256, false, false, LIN_OUT>(m, p, "linear_fwd", st)
-              : linear_launch<128, false, false, LIN_OUT>(m, p, "linear_fwd", st);
+  return lin_out<false>(shape, x, ldx, w, ldw, M, N, K, p, ws, "linear_fwd", (cudaStream_t)stream);
 }
 
 extern "C" size_t jenga_linear_bwd_workspace_bytes(int M, int N, int K, jenga_activation act) {
@@ -437,26 +387,13 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
       JENGA_LAUNCH_CHECK();
     }
   }
-  const int pairs = sm_count() / 2;
   if (dx) {
     LinArgs p{};
-    p.R = M;
-    p.C = K;
-    p.m = M;
-    p.nkb = (N + 63) / 64;
-    p.passes = 1;
     p.n_kept = n_kept;
     p.blk = blk;
     p.out = dx;
     p.ldo = ldd;
-    LinMats m;
-    JENGA_TRY(make_tmap_bf16(&m.a, dz, M, N, ldz, 128));
-    JENGA_TRY(make_tmap_bf16(&m.b, w, N, K, ldw, 64));
-    m.a2 = m.a3 = m.tail = m.out = m.pre = m.a;
-    p.out_tma = out_map(&m.out, dx, M, K, ldd);
-    const int64_t t256 = (int64_t)((M + 255) / 256) * ((K + 255) / 256);
-    JENGA_TRY((t256 >= pairs ? linear_launch<256, false, true, LIN_OUT>(m, p, "linear_dx", st)
-                             : linear_launch<128, false, true, LIN_OUT>(m, p, "linear_dx", st)));
+    JENGA_TRY(lin_out<true>(lin_shape(M, K, N), dz, ldz, w, ldw, M, K, N, p, W.dxpart, "linear_dx", st));
   }
   if (dw) {
     LinArgs p{};
@@ -464,6 +401,7 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
     p.C = K;
     p.m = M;
     p.nkb = (M + 63) / 64;
+    p.ksplit = 1;
     p.passes = parts;
     p.n_kept = n_kept;
     p.blk = blk;
@@ -489,8 +427,8 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
     }
     p.out_tma = is16(dw) && lddw % 4 == 0 && make_tmap_f32(&m.out, dw, N, K, lddw, 32) == JENGA_OK;
     const int64_t t256 = (int64_t)((N + 255) / 256) * ((K + 255) / 256);
-    JENGA_TRY((t256 >= pairs ? linear_launch<256, true, true, LIN_GRAD>(m, p, "linear_dw", st)
-                             : linear_launch<128, true, true, LIN_GRAD>(m, p, "linear_dw", st)));
+    JENGA_TRY((t256 >= sm_count() / 2 ? linear_launch<256, true, true, LIN_GRAD, false>(m, p, "linear_dw", st)
+                                      : linear_launch<128, true, true, LIN_GRAD, false>(m, p, "linear_dw", st)));
   }
   return JENGA_OK;
 }

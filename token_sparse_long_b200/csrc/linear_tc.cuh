@@ -12,6 +12,10 @@
 // B's rows per 64-deep k-block, and one tcgen05.mma (cta_group::2, M 256) issued by the
 // leader reads both CTAs' shared memory, so each SM moves half of the B tile it would alone.
 // Accumulators (128 lanes x BN columns per CTA) are double buffered in tensor memory.
+// With few rows of x (SWAP) the operands change places -- the weights are the 256-row side,
+// A = w or w^T, and x or dz the narrow one -- so that the weights, which are all the traffic,
+// spread over every SM; and a product with few tiles splits its reduction (ksplit) into fp32
+// partial products that linear_finish adds in order.
 // 320 threads per CTA:
 //   warp 0      TMA producer (both CTAs; completion counted on the leader's full barrier)
 //   warp 1      allocates tensor memory; in the leader one lane issues the MMAs and commits
@@ -43,6 +47,8 @@ constexpr int LT_CHUNK = 16;
 struct LinArgs {
   int R, C, nkb;                  // rows, columns, k-blocks of one pass over the reduction
   int m;                          // host bound on the rows of x (R, or the reduction of LIN_GRAD)
+  int ksplit;                     // LIN_OUT: ranges of k-blocks; above 1 the tiles go to `part`
+  float* part;                    // [ksplit][rows of x][columns of w's side] fp32
   int passes;                     // LIN_GRAD: 3 = A is held in three parts, one pass over the rows each
   const int32_t* n_kept;          // device count of valid blocks of x's rows (nullable)
   int blk;
@@ -59,14 +65,15 @@ struct LinArgs {
   int tail;                       // LIN_GRAD: the last partial k-block comes from the tail copy of x
 };
 
-template <int BN>
+template <int BN, bool SWAP>
 struct LinSmem {
-  static constexpr int STAGES = 5;
+  // narrow tiles move little per k-block: more of them in flight (about 180 KB an SM)
+  static constexpr int STAGES = SWAP ? (BN >= 128 ? 8 : 10) : (BN >= 256 ? 5 : 6);
   static constexpr int A_BYTES = 128 * 64 * 2;
   static constexpr int B_BYTES = BN / 2 * 64 * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int STG_OFF = STAGES * STAGE_BYTES;
-  static constexpr int STG_BYTES = 8 * 2 * 4096;  // two 32-row x 128-byte tiles per epilogue warp
+  static constexpr int STG_BYTES = SWAP ? 0 : 8 * 2 * 4096;  // two 32-row x 128-byte tiles per epilogue warp
   static constexpr int BAR_OFF = STG_OFF + STG_BYTES;
   static constexpr int TOTAL = BAR_OFF + 256 + 1024;
   static_assert(TOTAL <= 232448, "shared memory per CTA");
@@ -146,12 +153,37 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   return 1.f;
 }
 
-template <int BN, bool AMN, bool BMN, int MODE>
+// One output element from z = product + bias: pre, activation, residual, rounding.
+__device__ __forceinline__ void lin_finish(const LinArgs& p, int m, int n, float z) {
+  if (p.pre) p.pre[(int64_t)m * p.ldp + n] = __float2bfloat16_rn(z);
+  z = act_value(z, p.act);
+  if (p.residual) z += __bfloat162float(p.residual[(int64_t)m * p.ldr + n]);
+  reinterpret_cast<bf16*>(p.out)[(int64_t)m * p.ldo + n] = __float2bfloat16_rn(z);
+}
+
+// out = the epilogue of the partial products added in order; one column per thread, row y.
+__global__ void __launch_bounds__(256) linear_finish_kernel(LinArgs p, int N) {
+  const int m = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= N || m >= valid_rows(RowMap{nullptr, p.n_kept, p.blk, 0, p.m})) return;
+  const float* q = p.part + (int64_t)m * N + n;
+  float z = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.ksplit; ++s) z += q[(int64_t)s * p.m * N];
+  if (p.bias) {
+    float b;
+    load_params<1>(p.bias, p.bias_bf16, n, 0.f, &b);
+    z += b;
+  }
+  lin_finish(p, m, n, z);
+}
+
+template <int BN, bool AMN, bool BMN, int MODE, bool SWAP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                      const __grid_constant__ CUtensorMap tmA3, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmTail, const __grid_constant__ CUtensorMap tmOut,
                      const __grid_constant__ CUtensorMap tmPre, LinArgs p) {
-  using L = LinSmem<BN>;
+  using L = LinSmem<BN, SWAP>;
+  static_assert(!(BMN && BN < 128), "an MN-major B half is at least one 64-wide box");
   constexpr int ST = L::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -164,15 +196,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-  // LIN_OUT: the valid rows bound the row tiles; LIN_GRAD: they are the reduction
+  // LIN_OUT: the valid rows of x bound the row tiles (the column tiles with SWAP); LIN_GRAD: they
+  // are the reduction
   const int valid = valid_rows(RowMap{nullptr, p.n_kept, p.blk, 0, p.m});
-  const int rows = MODE == LIN_OUT ? valid : p.R;
+  const int rows = MODE == LIN_OUT && !SWAP ? valid : p.R;
+  const int cols = SWAP ? valid : p.C;
   const int nkb1 = MODE == LIN_OUT ? p.nkb : (valid + 63) / 64;
-  const int nkb = nkb1 * (MODE == LIN_GRAD ? p.passes : 1);
-  const int ntr = (rows + 255) / 256, ntc = (p.C + BN - 1) / BN;
-  const int ntiles = ntr * ntc;
+  const int nkb_all = nkb1 * (MODE == LIN_GRAD ? p.passes : 1);
+  const int ntr = (rows + 255) / 256, ntc = (cols + BN - 1) / BN;
+  const int ksplit = MODE == LIN_OUT ? p.ksplit : 1;
+  const int ntiles = ntr * ntc * ksplit;
   if (cluster >= ntiles) return;  // uniform over the cluster
-  auto tile_at = [&](int t, int& r0, int& c0) {
+  // work tile t: output tile t / ksplit, k-blocks [lo, hi) of range t % ksplit
+  auto tile_at = [&](int t, int& r0, int& c0, int& lo, int& hi) {
+    const int ks = t % ksplit;
+    t /= ksplit;
+    lo = (int)((int64_t)nkb_all * ks / ksplit);
+    hi = (int)((int64_t)nkb_all * (ks + 1) / ksplit);
     const int band = t / (LT_BAND * ntc), rem = t - band * LT_BAND * ntc;
     const int gm = min(LT_BAND, ntr - band * LT_BAND);
     r0 = (band * LT_BAND + rem % gm) * 256;
@@ -207,11 +247,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     int g = 0;
     bool ok = true;
     for (int t = cluster; ok && t < ntiles; t += nclusters) {
-      int r0, c0;
-      tile_at(t, r0, c0);
+      int r0, c0, lo, hi;
+      tile_at(t, r0, c0, lo, hi);
       r0 += rank * 128;
       c0 += rank * (BN / 2);
-      for (int kb = 0; kb < nkb; ++kb, ++g) {
+      for (int kb = lo; kb < hi; ++kb, ++g) {
         const int s = g % ST;
         if (g >= ST && !__all_sync(0xffffffffu, pair_wait(&empty[s], ((g / ST) - 1) & 1))) {
           ok = false;
@@ -256,9 +296,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     bool ok = true;
     int g = 0, it = 0;
     for (int t = cluster; ok && t < ntiles; t += nclusters) {
-      for (int kb = 0; ok && kb < nkb; ++kb, ++g) {
-        const bool first = MODE == LIN_GRAD ? kb % LT_CHUNK == 0 : kb == 0;
-        const bool last = kb == nkb - 1 || (MODE == LIN_GRAD && kb % LT_CHUNK == LT_CHUNK - 1);
+      int r0, c0, lo, hi;
+      tile_at(t, r0, c0, lo, hi);
+      for (int kb = lo; ok && kb < hi; ++kb, ++g) {
+        const bool first = MODE == LIN_GRAD ? kb % LT_CHUNK == 0 : kb == lo;
+        const bool last = kb == hi - 1 || (MODE == LIN_GRAD && kb % LT_CHUNK == LT_CHUNK - 1);
         const int buf = it & 1;
         if (first && it >= 2 && !__all_sync(0xffffffffu, pair_wait(&acc_empty[buf], ((it >> 1) - 1) & 1))) {
           ok = false;
@@ -304,8 +346,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     };
     int it = 0;
     for (int t = cluster; t < ntiles; t += nclusters) {
-      int r0, c0;
-      tile_at(t, r0, c0);
+      int r0, c0, lo, hi;
+      tile_at(t, r0, c0, lo, hi);
       const int rw = r0 + (int)rank * 128 + quarter * 32;  // the warp's first row
       const int r = rw + lane;
       const int cw = c0 + half * (BN / 2);                 // the warp's first column
@@ -314,6 +356,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         const bool ok = __all_sync(0xffffffffu, pair_wait(&acc_full[buf], (it >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
+        if constexpr (SWAP) {
+          // lane = row of w = column n of the output; the warp's tokens go by in steps of 16
+#pragma unroll 1
+          for (int cc = 0; cc < BN / 32; ++cc) {
+            const int m0 = cw + cc * 16;
+            uint32_t raw[16];
+            __syncwarp();  // the load below is collective
+            tmem_ld16_nowait(lane_base + buf * BN + cc * 16, raw);
+            tmem_wait_ld();
+            if (cc == BN / 32 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(empty_leader[buf]);
+            }
+            if (r >= rows) continue;
+            if (ksplit > 1) {
+              float* o = p.part + ((int64_t)(t % ksplit) * p.m + m0) * rows + r;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (m0 + i < cols) o[(int64_t)i * rows] = __uint_as_float(raw[i]);
+              continue;
+            }
+            float b = 0.f;
+            if (p.bias) load_params<1>(p.bias, p.bias_bf16, r, 0.f, &b);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int m = m0 + i;
+              if (m < cols) lin_finish(p, m, r, __uint_as_float(raw[i]) + b);
+            }
+          }
+          ++it;
+          continue;
+        }
         const bool whole = rw + 32 <= rows;
 #pragma unroll 1
         for (int cc = 0; cc < BN / 128; ++cc) {
@@ -329,6 +404,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           }
           if (n >= p.C || rw >= rows) continue;
           const bool full_cols = n + 64 <= p.C;
+          if (ksplit > 1) {
+            if (r < rows) {
+              float* o = p.part + ((int64_t)(t % ksplit) * p.m + r) * p.C + n;
+              if (full_cols && (p.C & 3) == 0) {
+#pragma unroll
+                for (int i = 0; i < 64; i += 4)
+                  *reinterpret_cast<uint4*>(o + i) = make_uint4(raw[i], raw[i + 1], raw[i + 2], raw[i + 3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                  if (n + i < p.C) o[i] = __uint_as_float(raw[i]);
+              }
+            }
+            continue;
+          }
           float v[64];
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(raw[i]);
@@ -417,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < BN / 2; ++i) acc[i] = 0.f;
         bool ok = true;
-        for (int kb = 0; kb < nkb; kb += LT_CHUNK) {
+        for (int kb = 0; kb < hi; kb += LT_CHUNK) {
           const int buf = it & 1;
           ok = __all_sync(0xffffffffu, pair_wait(&acc_full[buf], (it >> 1) & 1));
           if (!ok) break;
