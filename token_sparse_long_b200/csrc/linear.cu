@@ -150,9 +150,10 @@ static bool out_map(CUtensorMap* map, const void* base, int rows, int cols, int6
 }
 
 // Shape of a forward or dx product [M, N] over `red`: operands swapped (and the narrow side's
-// tile), tile width, ranges of the reduction.  Costs in k-blocks of a 256-wide tile (530 clocks;
-// a 128-wide one takes 390: the issue of its four MMAs and the loads do not halve), `fill` for
-// a tile's first loads and its epilogue; a split adds the pass over the partial products.
+// tile), tile width, ranges of the reduction.  Costs in k-blocks of a 256-wide tile (530 clocks
+// measured; a 128-wide tile's take 390 and a narrow swapped one's about as long, since the issue
+// of the four MMAs does not shrink).  A further tile of a cluster costs its epilogue's start;
+// a split adds the pass over the partial products: a launch, and 0.8 MB a k-block of time.
 struct LinShape {
   bool swap;
   int bn, ksplit;
@@ -163,11 +164,11 @@ static LinShape lin_shape(int M, int N, int red) {
   double cost = 1e300;
   auto consider = [&](bool swap, int bn) {
     const int64_t tiles = (int64_t)(((swap ? N : M) + 255) / 256) * (((swap ? M : N) + bn - 1) / bn);
-    const double per = swap ? (bn >= 128 ? 0.75 : 0.55) : (bn >= 256 ? 1.0 : 0.75), fill = 4.0;
+    const double per = swap || bn < 256 ? 0.75 : 1.0, fill = 1.5;
     for (int s = 1; s <= 16 && s <= 1 + nkb / 8; ++s) {
       const double waves = (double)((tiles * s + pairs - 1) / pairs);
       double c = waves * (per * ((nkb + s - 1) / s) + fill);
-      if (s > 1) c += 10.0 + (double)s * M * N * 8.0 / 2.0e6;  // a launch; 2 MB a k-block of time through L2
+      if (s > 1) c += 12.0 + (double)s * M * N * 8.0 / 0.8e6;
       if (c < cost * 0.97) {
         cost = c;
         best = LinShape{swap, bn, s};
@@ -221,7 +222,10 @@ static jenga_status lin_out(const LinShape& s, const void* x, int64_t ldx, const
   }
   if (s.ksplit > 1) {
     const int ps = prof_begin("linear_finish", st);
-    linear_finish_kernel<<<dim3((N + 255) / 256, M), 256, 0, st>>>(p, N);
+    if (N % 4 == 0)
+      linear_finish_kernel<4><<<dim3((N + 511) / 512, M), 128, 0, st>>>(p, N);
+    else
+      linear_finish_kernel<1><<<dim3((N + 127) / 128, M), 128, 0, st>>>(p, N);
     prof_end(ps, st);
     JENGA_LAUNCH_CHECK();
   }

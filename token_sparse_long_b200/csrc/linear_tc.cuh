@@ -74,7 +74,9 @@ struct LinSmem {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int STG_OFF = STAGES * STAGE_BYTES;
   static constexpr int STG_BYTES = SWAP ? 0 : 8 * 2 * 4096;  // two 32-row x 128-byte tiles per epilogue warp
-  static constexpr int BAR_OFF = STG_OFF + STG_BYTES;
+  static constexpr int BIAS_OFF = STG_OFF + STG_BYTES;
+  static constexpr int BIAS_BYTES = SWAP ? 0 : BN * 4;  // the tile's bias, fp32
+  static constexpr int BAR_OFF = BIAS_OFF + BIAS_BYTES;
   static constexpr int TOTAL = BAR_OFF + 256 + 1024;
   static_assert(TOTAL <= 232448, "shared memory per CTA");
 };
@@ -142,6 +144,19 @@ __device__ __forceinline__ float act_value(float z, int act) {
   if (act == JENGA_ACT_SILU) return z / (1.f + __expf(-z));
   return z;
 }
+template <int N>
+__device__ __forceinline__ void act_values(float* v, int act) {
+  if (act == JENGA_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_value(v[i], JENGA_ACT_RELU);
+  } else if (act == JENGA_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_value(v[i], JENGA_ACT_GELU);
+  } else if (act == JENGA_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_value(v[i], JENGA_ACT_SILU);
+  }
+}
 __device__ __forceinline__ float act_slope(float z, int act) {
   if (act == JENGA_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if (act == JENGA_ACT_GELU)
@@ -161,20 +176,37 @@ __device__ __forceinline__ void lin_finish(const LinArgs& p, int m, int n, float
   reinterpret_cast<bf16*>(p.out)[(int64_t)m * p.ldo + n] = __float2bfloat16_rn(z);
 }
 
-// out = the epilogue of the partial products added in order; one column per thread, row y.
-__global__ void __launch_bounds__(256) linear_finish_kernel(LinArgs p, int N) {
-  const int m = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+// out = the epilogue of the partial products added in order: V columns per thread (four when the
+// partial rows are 16-byte aligned), row y of the grid.
+template <int V>
+__global__ void __launch_bounds__(128) linear_finish_kernel(LinArgs p, int N) {
+  const int m = blockIdx.y, n = (blockIdx.x * 128 + threadIdx.x) * V;
   if (n >= N || m >= valid_rows(RowMap{nullptr, p.n_kept, p.blk, 0, p.m})) return;
   const float* q = p.part + (int64_t)m * N + n;
-  float z = 0.f;
+  float z[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) z[e] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < p.ksplit; ++s) z += q[(int64_t)s * p.m * N];
-  if (p.bias) {
-    float b;
-    load_params<1>(p.bias, p.bias_bf16, n, 0.f, &b);
-    z += b;
+  for (int s = 0; s < p.ksplit; ++s) {
+    if constexpr (V == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(q + (int64_t)s * p.m * N);
+      z[0] += f.x;
+      z[1] += f.y;
+      z[2] += f.z;
+      z[3] += f.w;
+    } else {
+      z[0] += q[(int64_t)s * p.m * N];
+    }
   }
-  lin_finish(p, m, n, z);
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if (p.bias) {
+      float b;
+      load_params<1>(p.bias, p.bias_bf16, n + e, 0.f, &b);
+      z[e] += b;
+    }
+    lin_finish(p, m, n + e, z[e]);
+  }
 }
 
 template <int BN, bool AMN, bool BMN, int MODE, bool SWAP>
@@ -335,6 +367,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     uint8_t* stg = smem + L::STG_OFF + (warp - 2) * 2 * 4096;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
     const uint32_t empty_leader[2] = {map_rank(smem_u32(&acc_empty[0]), 0), map_rank(smem_u32(&acc_empty[1]), 0)};
+    float* s_bias = reinterpret_cast<float*>(smem + L::BIAS_OFF);
+    bool alive = true;
     int nst = 0;
     auto stage_wait = [&] {  // the store that last read staging tile nst & 1 is done
       if (lane == 0 && nst >= 2) bulk_wait_group_read<1>();
@@ -353,8 +387,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       const int cw = c0 + half * (BN / 2);                 // the warp's first column
       if (MODE == LIN_OUT) {
         const int buf = it & 1;
+        if (!SWAP) {
+          // the tile's bias goes through shared memory: read per row from global memory its 64
+          // loads a chunk cost 25 us at the end of a product.  A warp that timed out takes the
+          // others with it here (the barrier carries the AND of `alive`).
+          if (!bar_and(alive, 1, 256)) break;
+          const int q = (warp - 2) * 32 + lane;
+          float bv = 0.f;
+          if (q < BN) {
+            if (p.bias && c0 + q < p.C) load_params<1>(p.bias, p.bias_bf16, c0 + q, 0.f, &bv);
+            s_bias[q] = bv;
+          }
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+        // the residual's first chunk is on its way before the product is ready
+        const bool res_vec = !SWAP && p.residual && (p.ldr & 7) == 0 && aligned16_dev(p.residual);
+        uint4 rq[8];
+        auto fetch_res = [&](int n) {
+          if (res_vec && r < rows && n + 64 <= p.C) {
+            const uint4* q = reinterpret_cast<const uint4*>(p.residual + (int64_t)r * p.ldr + n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rq[i] = q[i];
+          }
+        };
+        if (!SWAP) fetch_res(cw);
         const bool ok = __all_sync(0xffffffffu, pair_wait(&acc_full[buf], (it >> 1) & 1));
-        if (!ok) break;
+        if (!ok) {
+          if (SWAP) break;
+          alive = false;
+          continue;
+        }
         tc_fence_after();
         if constexpr (SWAP) {
           // lane = row of w = column n of the output; the warp's tokens go by in steps of 16
@@ -423,22 +485,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(raw[i]);
           if (p.bias) {
-            if (full_cols && aligned16_dev(p.bias)) {
+            const float4* bq = reinterpret_cast<const float4*>(s_bias + half * (BN / 2) + cc * 64);
 #pragma unroll
-              for (int i = 0; i < 64; i += 8) {
-                float b[8];
-                load_params<8>(p.bias, p.bias_bf16, n + i, 0.f, b);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i + e] += b[e];
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 64; ++i)
-                if (n + i < p.C) {
-                  float b;
-                  load_params<1>(p.bias, p.bias_bf16, n + i, 0.f, &b);
-                  v[i] += b;
-                }
+            for (int i = 0; i < 16; ++i) {
+              const float4 b = bq[i];
+              v[4 * i] += b.x;
+              v[4 * i + 1] += b.y;
+              v[4 * i + 2] += b.z;
+              v[4 * i + 3] += b.w;
             }
           }
           if (p.pre) {
@@ -461,26 +515,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
                 if (n + i < p.C) o[i] = __float2bfloat16_rn(v[i]);
             }
           }
-          if (p.act != JENGA_ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] = act_value(v[i], p.act);
-          }
+          act_values<64>(v, p.act);
           if (p.residual && r < rows) {
-            const bf16* q = p.residual + (int64_t)r * p.ldr + n;
-            if (full_cols && (p.ldr & 7) == 0 && aligned16_dev(p.residual)) {
+            if (res_vec && full_cols) {
 #pragma unroll
-              for (int i = 0; i < 64; i += 32) {
-                float f[32];
-                load_bf16x32(q + i, f);
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t w[4] = {rq[i].x, rq[i].y, rq[i].z, rq[i].w};
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[i + e] += f[e];
+                for (int e = 0; e < 4; ++e) {
+                  v[8 * i + 2 * e] += __uint_as_float(w[e] << 16);
+                  v[8 * i + 2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+                }
               }
             } else {
+              const bf16* q = p.residual + (int64_t)r * p.ldr + n;
 #pragma unroll
               for (int i = 0; i < 64; ++i)
                 if (n + i < p.C) v[i] += __bfloat162float(q[i]);
             }
           }
+          if (cc + 1 < BN / 128) fetch_res(n + 64);
           if (whole && p.out_tma) {
             stage_wait();
             uint8_t* tb = stg + (nst & 1) * 4096;
