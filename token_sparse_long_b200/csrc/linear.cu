@@ -124,6 +124,127 @@ __global__ void __launch_bounds__(256) linear_tail_kernel(const bf16* __restrict
     tail[r * ldt + c] = r0 + r < valid ? x[(int64_t)(r0 + r) * ldx + c] : __float2bfloat16_rn(0.f);
 }
 
+// Forward for one or two rows of x: the weights are the whole traffic, read once.  Each CTA takes
+// a consecutive share of w's rows and streams them through a ring of whole rows in shared memory
+// (bulk copies by a warp of their own, up to 190 KB in flight an SM whatever the others do).
+// A group of G warps takes a row: it holds its slice of x as fp32 in registers (NV vectors of
+// eight a thread), so a weight is read from shared memory once and used MT times, and with G = 1
+// eight rows are reduced side by side (all eight warps on one row: 400 clocks a row).  The
+// sums of GV_BATCH rows at a time meet in shared memory, where the epilogue runs.  fp32
+// products and sums.  One row of 4096 into 32000: 52 us, 5.1 TB/s; into 11008: 23 us (the tensor
+// core kernel with its second launch: 24, and 18 against 13 us into 4096); at four rows the
+// products bound it (78 us) and the tensor cores win.
+constexpr int GV_BATCH = 64;
+constexpr int GV_MAX_STAGES = 64;
+template <int MT, int NV>
+__global__ void __launch_bounds__(288)
+    linear_rows_kernel(const bf16* __restrict__ w, int64_t ldw, const bf16* __restrict__ x, int64_t ldx, int N, int K,
+                       int G, int stages, LinArgs p) {
+  extern __shared__ __align__(128) uint8_t s_w[];
+  __shared__ uint64_t s_full[GV_MAX_STAGES], s_empty[GV_MAX_STAGES];
+  __shared__ float s_part[2][GV_BATCH][MT][8];
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int valid = valid_rows(RowMap{nullptr, p.n_kept, p.blk, 0, p.m});
+  const int lo = (int)((int64_t)N * blockIdx.x / gridDim.x), hi = (int)((int64_t)N * (blockIdx.x + 1) / gridDim.x);
+  const uint32_t row_bytes = (uint32_t)K * 2;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], G);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (valid == 0) return;
+  if (warp == 8) {
+    // ---------------- producer
+    int s = 0, ph = 1;  // the first lap finds every stage free
+    for (int n = lo; n < hi; ++n) {
+      if (!__all_sync(0xffffffffu, poll_wait(&s_empty[s], ph, SITE_LINEAR))) return;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&s_full[s], row_bytes);
+        bulk_load_1d(s_w + (size_t)s * row_bytes, w + (int64_t)n * ldw, row_bytes, &s_full[s]);
+      }
+      __syncwarp();
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    return;
+  }
+  // ---------------- eight warps of dot products
+  const int groups = 8 / G, grp = warp / G, gwarp = warp - grp * G;
+  const int nvec = K / 8, v0 = gwarp * 32 + lane, step = G * 32;
+  float xf[MT][NV][8];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      RowVec<bf16, 8> v;
+      v.zero();
+      if (m < valid && v0 + i * step < nvec) v.load(x + (int64_t)m * ldx + (int64_t)(v0 + i * step) * 8);
+      v.get(xf[m][i]);
+    }
+  bool ok = true;
+  int s = grp, ph = 0;  // the group's stage (stages >= groups)
+  for (int b0 = lo, bi = 0; b0 < hi; b0 += GV_BATCH, bi ^= 1) {
+    const int b1 = min(b0 + GV_BATCH, hi);
+    for (int n = b0 + grp; n < b1; n += groups) {
+      ok = __all_sync(0xffffffffu, poll_wait(&s_full[s], ph, SITE_LINEAR));
+      if (!ok) break;
+      const uint8_t* row = s_w + (size_t)s * row_bytes + v0 * 16;
+      float acc[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (v0 + i * step < nvec) {
+          RowVec<bf16, 8> v;
+          float f[8];
+          v.r = *reinterpret_cast<const uint4*>(row + i * step * 16);
+          v.get(f);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[m][e & 1] = fmaf(f[e], xf[m][i][e], acc[m][e & 1]);
+        }
+      }
+      __syncwarp();  // every lane has read the row
+      if (lane == 0) mbar_arrive(&s_empty[s]);
+      float t[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) t[m] = acc[m][0] + acc[m][1];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) t[m] += __shfl_xor_sync(0xffffffffu, t[m], o);
+      if (lane == 0) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) s_part[bi][n - b0][m][gwarp] = t[m];
+      }
+      s += groups;
+      if (s >= stages) {
+        s -= stages;
+        ph ^= 1;
+      }
+    }
+    if (!bar_and(ok, 1, 256)) return;  // a warp that timed out takes the others with it
+    for (int i = threadIdx.x; i < (b1 - b0) * MT; i += 256) {
+      const int m = i / (b1 - b0), q = i - m * (b1 - b0);
+      if (m >= valid) continue;
+      float z = 0.f;
+      for (int k = 0; k < G; ++k) z += s_part[bi][q][m][k];
+      if (p.bias) {
+        float b;
+        load_params<1>(p.bias, p.bias_bf16, b0 + q, 0.f, &b);
+        z += b;
+      }
+      lin_finish(p, m, b0 + q, z);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ host
 struct LinMats {
   CUtensorMap a, a2, a3, b, tail, out, pre;
@@ -186,6 +307,10 @@ static LinShape lin_shape(int M, int N, int red) {
 static size_t lin_part_bytes(const LinShape& s, int M, int N) {
   return s.ksplit > 1 ? (size_t)s.ksplit * M * N * sizeof(float) + 256 : 0;
 }
+
+// Is the forward a pass over the rows of w (linear_rows)?  x as fp32 has to fit the registers of eight
+// warps; rows of w are copied whole, in multiples of 16 bytes.
+static bool lin_rows_ok(int M, int K) { return M <= 2 && K % 8 == 0 && K <= 16384; }
 
 // forward or dx: x side [M, red] (K-major), weight side [N, red] K-major or (WMN) [red, N]
 template <bool WMN>
@@ -281,7 +406,7 @@ using namespace jenga;
 
 extern "C" size_t jenga_linear_fwd_workspace_bytes(int M, int N, int K) {
   if (M < 1 || N < 1 || K < 1) return 0;
-  return lin_part_bytes(lin_shape(M, N, K), M, N);
+  return lin_rows_ok(M, K) ? 0 : lin_part_bytes(lin_shape(M, N, K), M, N);
 }
 
 extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
@@ -304,7 +429,7 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
                       alias_ok(pre, ldp, np, residual, ldr, nr, false),
                   "jenga_linear_fwd: an output overlaps an input (only y = residual, the same matrix, is allowed)");
   const LinShape shape = lin_shape(M, N, K);
-  const size_t need = lin_part_bytes(shape, M, N);
+  const size_t need = jenga_linear_fwd_workspace_bytes(M, N, K);
   if (need && (!ws || ws_bytes < need))
     return fail(JENGA_EWORKSPACE, "jenga_linear_fwd: workspace %zu < %zu", ws ? ws_bytes : (size_t)0, need);
   LinArgs p{};
@@ -319,7 +444,34 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
   p.ldo = ldy;
   p.pre = (bf16*)pre;
   p.ldp = ldp;
-  return lin_out<false>(shape, x, ldx, w, ldw, M, N, K, p, ws, "linear_fwd", (cudaStream_t)stream);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (lin_rows_ok(M, K)) {
+    p.m = M;
+    const int row = K * 2, room = 192 * 1024;
+    int stages = room / row;
+    stages = stages < GV_MAX_STAGES ? stages : GV_MAX_STAGES;
+    // 128 registers of x a thread at the most; as few warps a row as that allows
+    const int most = 16 / M;
+    int G = 1;
+    while ((K / 8 + 32 * G - 1) / (32 * G) > most) G *= 2;
+    const int nv = (K / 8 + 32 * G - 1) / (32 * G);
+    const unsigned grid = (unsigned)(N < sm_count() ? N : sm_count());
+    const int ps = prof_begin("linear_rows", st);
+    auto go = [&](auto kernel) {
+      const cudaError_t e = allow_smem((const void*)kernel, room);
+      if (e == cudaSuccess)
+        kernel<<<grid, 288, (size_t)stages * row, st>>>((const bf16*)w, ldw, (const bf16*)x, ldx, N, K, G, stages, p);
+      return e;
+    };
+    JENGA_CUDA_TRY(M == 1   ? (nv <= 4   ? go(linear_rows_kernel<1, 4>)
+                               : nv <= 8 ? go(linear_rows_kernel<1, 8>)
+                                         : go(linear_rows_kernel<1, 16>))
+                            : (nv <= 4 ? go(linear_rows_kernel<2, 4>) : go(linear_rows_kernel<2, 8>)));
+    prof_end(ps, st);
+    JENGA_LAUNCH_CHECK();
+    return JENGA_OK;
+  }
+  return lin_out<false>(shape, x, ldx, w, ldw, M, N, K, p, ws, "linear_fwd", st);
 }
 
 extern "C" size_t jenga_linear_bwd_workspace_bytes(int M, int N, int K, jenga_activation act) {

@@ -252,6 +252,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   };
 
   if (threadIdx.x == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -272,10 +274,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   if (warp == 0) {
     // ---------------- TMA producer (the warp stays converged and elects a lane to issue: from a
     // divergent lane each copy or MMA took about 100 clocks to issue, 700 per k-block for 530)
-    if (elect_one()) {
-      prefetch_tmap(&tmA);
-      prefetch_tmap(&tmB);
-    }
     int g = 0;
     bool ok = true;
     for (int t = cluster; ok && t < ntiles; t += nclusters) {
@@ -440,13 +438,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
                 if (m0 + i < cols) o[(int64_t)i * rows] = __uint_as_float(raw[i]);
               continue;
             }
-            float b = 0.f;
+            float b = 0.f, v[16];
             if (p.bias) load_params<1>(p.bias, p.bias_bf16, r, 0.f, &b);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int m = m0 + i;
-              if (m < cols) lin_finish(p, m, r, __uint_as_float(raw[i]) + b);
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(raw[i]) + b;
+            if (p.pre) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (m0 + i < cols) p.pre[(int64_t)(m0 + i) * p.ldp + r] = __float2bfloat16_rn(v[i]);
             }
+            act_values<16>(v, p.act);
+            if (p.residual) {
+              float e[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                e[i] = m0 + i < cols ? __bfloat162float(p.residual[(int64_t)(m0 + i) * p.ldr + r]) : 0.f;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += e[i];
+            }
+            bf16* o = reinterpret_cast<bf16*>(p.out) + (int64_t)m0 * p.ldo + r;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (m0 + i < cols) o[(int64_t)i * p.ldo] = __float2bfloat16_rn(v[i]);
           }
           ++it;
           continue;
