@@ -452,19 +452,25 @@ def jenga_layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, idx=None, n_kept=Non
     try:
         ldx = _mat(x, "x")
         S, h = x.shape
-        rows = _rows_arg(idx, n_kept, blk, n_kept_max, S)
-        _vec(gamma, "gamma", h)
-        _vec(beta, "beta", h)
-        if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-            raise TypeError("gamma and beta differ in dtype")
+        rows = S if idx is None and n_kept is None else _rows_arg(idx, n_kept, blk, n_kept_max, S)
         w = gamma if gamma is not None else beta
+        if gamma is not None:
+            _vec(gamma, "gamma", h)
+        if beta is not None:
+            _vec(beta, "beta", h, w.dtype)
         dt = _dt(x)
-        y = x.new_empty((rows, h)) if out is None else out
-        mean = x.new_empty(rows, dtype=torch.float32) if mean is None else mean
-        rstd = x.new_empty(rows, dtype=torch.float32) if rstd is None else rstd
-        ldy = h if out is None else _mat(y, "out", h, rows, x.dtype)
-        _vec(mean, "mean", rows, torch.float32)
-        _vec(rstd, "rstd", rows, torch.float32)
+        if out is None:
+            y, ldy = x.new_empty((rows, h)), h
+        else:
+            y, ldy = out, _mat(out, "out", h, rows, x.dtype)
+        if mean is None:
+            mean = x.new_empty(rows, dtype=torch.float32)
+        else:
+            _vec(mean, "mean", rows, torch.float32)
+        if rstd is None:
+            rstd = x.new_empty(rows, dtype=torch.float32)
+        else:
+            _vec(rstd, "rstd", rows, torch.float32)
         check(load().jenga_layernorm_fwd(x.data_ptr(), ldx, S, h, _ptr(idx), _ptr(n_kept), blk, rows, _ptr(gamma),
                                          _ptr(beta), _dt(w) if w is not None else F32, eps, dt, y.data_ptr(), ldy,
                                          mean.data_ptr(), rstd.data_ptr(), s))
@@ -478,30 +484,35 @@ def jenga_layernorm_bwd(dy, x, mean, rstd, gamma=None, idx=None, n_kept=None, bl
     """Gradients of jenga_layernorm_fwd: dy [rows, h] compact; x, dres and dx like the forward's x
     -> (dx, dgamma fp32 [h], dbeta fp32 [h]).
 
-    dres: gradient of the residual branch, added into dx (dx may be dres: in place).  With idx
-    and no dx given, rows outside the list are zero.  accumulate: add into the given dgamma and
+    dres: gradient of the residual branch, added into dx (dx may be dres: in place).  With idx or
+    n_kept and no dx given, rows outside the list are zero.  accumulate: add into the given dgamma and
     dbeta.  weight_grads=False skips both (None unless given)."""
     guard, s = _begin(stream, x, dy, mean, rstd, gamma, idx, n_kept, dres, dx, dgamma, dbeta, ws)
     try:
         ldx = _mat(x, "x")
         S, h = x.shape
-        rows = _rows_arg(idx, n_kept, blk, n_kept_max, S)
+        rows = S if idx is None and n_kept is None else _rows_arg(idx, n_kept, blk, n_kept_max, S)
         ldy = _mat(dy, "dy", h, rows, x.dtype)
-        _vec(gamma, "gamma", h)
+        if gamma is not None:
+            _vec(gamma, "gamma", h)
         _vec(mean, "mean", rows, torch.float32)
         _vec(rstd, "rstd", rows, torch.float32)
         dt = _dt(x)
         if dx is None:
-            dx = x.new_empty((S, h)) if idx is None else x.new_zeros((S, h))
-        ldd = _mat(dx, "dx", h, S, x.dtype)
+            dx, ldd = x.new_empty((S, h)) if idx is None and n_kept is None else x.new_zeros((S, h)), h
+        else:
+            ldd = _mat(dx, "dx", h, S, x.dtype)
         ldr = _mat(dres, "dres", h, S, x.dtype) if dres is not None else 0
-        if weight_grads:
-            if accumulate and (dgamma is None or dbeta is None):
-                raise ValueError("accumulate needs dgamma and dbeta")
-            dgamma = mean.new_empty(h) if dgamma is None else dgamma
-            dbeta = mean.new_empty(h) if dbeta is None else dbeta
-        _vec(dgamma, "dgamma", h, torch.float32)
-        _vec(dbeta, "dbeta", h, torch.float32)
+        if weight_grads and accumulate and (dgamma is None or dbeta is None):
+            raise ValueError("accumulate needs dgamma and dbeta")
+        if dgamma is not None:
+            _vec(dgamma, "dgamma", h, torch.float32)
+        elif weight_grads:
+            dgamma = mean.new_empty(h)
+        if dbeta is not None:
+            _vec(dbeta, "dbeta", h, torch.float32)
+        elif weight_grads:
+            dbeta = mean.new_empty(h)
         lib = load()
         if ws is None and (dgamma is not None or dbeta is not None):
             ws = x.new_empty(lib.jenga_layernorm_bwd_workspace_bytes(rows, h), dtype=torch.uint8)
@@ -532,7 +543,8 @@ def jenga_linear_fwd(x, w, bias=None, act="none", residual=None, n_kept=None, bl
         N = w.shape[0]
         if n_kept is not None:
             _rows_arg(None, n_kept, blk, None, M)
-        _vec(bias, "bias", N)
+        if bias is not None:
+            _vec(bias, "bias", N)
         ldr = _mat(residual, "residual", N, M, bf) if residual is not None else 0
         y = x.new_empty((M, N)) if out is None else out
         ldy = N if out is None else _mat(y, "out", N, M, bf)
@@ -574,12 +586,25 @@ def jenga_linear_bwd(dy, x, w, act="none", pre=None, n_kept=None, blk=1, need=("
         want_w, want_b = "dw" in need, "db" in need
         if accumulate and ((want_w and dw is None) or (want_b and db is None)):
             raise ValueError("accumulate needs dw and db")
-        dx = (x.new_empty((M, K)) if dx is None else dx) if "dx" in need else None
-        dw = (x.new_empty((N, K), dtype=f32) if dw is None else dw) if want_w else None
-        db = (x.new_empty(N, dtype=f32) if db is None else db) if want_b else None
-        ldd = _mat(dx, "dx", K, M, bf) if dx is not None else 0
-        lddw = _mat(dw, "dw", K, N, f32) if dw is not None else 0
-        _vec(db, "db", N, f32)
+        ldd, lddw = K, K
+        if "dx" not in need:
+            dx = None
+        elif dx is None:
+            dx = x.new_empty((M, K))
+        else:
+            ldd = _mat(dx, "dx", K, M, bf)
+        if not want_w:
+            dw = None
+        elif dw is None:
+            dw = x.new_empty((N, K), dtype=f32)
+        else:
+            lddw = _mat(dw, "dw", K, N, f32)
+        if not want_b:
+            db = None
+        elif db is None:
+            db = x.new_empty(N, dtype=f32)
+        else:
+            _vec(db, "db", N, f32)
         lib, a = load(), ACTIVATIONS[act]
         if ws is None:
             ws = x.new_empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, a), dtype=torch.uint8)

@@ -113,6 +113,19 @@ __global__ void __launch_bounds__(128) linear_db_reduce_kernel(const float* __re
   db[c] = accumulate ? db[c] + a : a;
 }
 
+// dw[r][c] (+)= the partial products added in order (row y of the grid)
+__global__ void __launch_bounds__(256) linear_dw_sum_kernel(const float* __restrict__ part, int splits, int N, int K,
+                                                            float* dw, int64_t ldw, int accumulate) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= K) return;
+  const float* q = part + (int64_t)blockIdx.y * K + c;
+  float a = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) a += q[(int64_t)s * N * K];
+  float* o = dw + (int64_t)blockIdx.y * ldw + c;
+  *o = accumulate ? *o + a : a;
+}
+
 // The rows of x past the last whole 64-row block, with zeros up to 64 rows (a device row count
 // can end inside x, whose later rows may hold anything).
 __global__ void __launch_bounds__(256) linear_tail_kernel(const bf16* __restrict__ x, int64_t ldx, int M, int K,
@@ -255,7 +268,7 @@ static jenga_status linear_launch(const LinMats& m, const LinArgs& p, const char
   using L = LinSmem<BN, SWAP>;
   auto kernel = linear_tc_kernel<BN, AMN, BMN, MODE, SWAP>;
   JENGA_CUDA_TRY(allow_smem((const void*)kernel, L::TOTAL));
-  const int64_t tiles = (int64_t)((p.R + 255) / 256) * ((p.C + BN - 1) / BN) * (MODE == LIN_OUT ? p.ksplit : 1);
+  const int64_t tiles = (int64_t)((p.R + 255) / 256) * ((p.C + BN - 1) / BN) * p.ksplit;
   const int pairs = sm_count() / 2;
   const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
   const int ps = prof_begin(name, st);
@@ -286,7 +299,7 @@ static LinShape lin_shape(int M, int N, int red) {
   auto consider = [&](bool swap, int bn) {
     const int64_t tiles = (int64_t)(((swap ? N : M) + 255) / 256) * (((swap ? M : N) + bn - 1) / bn);
     const double per = swap || bn < 256 ? 0.75 : 1.0, fill = 1.5;
-    for (int s = 1; s <= 16 && s <= 1 + nkb / 8; ++s) {
+    for (int s = 1; s <= (M < 65536 ? 16 : 1) && s <= 1 + nkb / 8; ++s) {  // linear_finish: a grid row per row
       const double waves = (double)((tiles * s + pairs - 1) / pairs);
       double c = waves * (per * ((nkb + s - 1) / s) + fill);
       if (s > 1) c += 12.0 + (double)s * M * N * 8.0 / 0.8e6;
@@ -370,9 +383,20 @@ static int dz_rows_per(int M, int N) {  // rows per chunk of linear_dz: about fo
 // parts that dz is held in: all of its 24 bits for dw after a smooth activation
 static int dz_parts(int act) { return act == JENGA_ACT_GELU || act == JENGA_ACT_SILU ? 3 : 1; }
 
+// ranges of dw's reduction when its tiles leave SM pairs idle (at least eight k-blocks each); the
+// sum over them then takes a pass of its own over N x K values, at most 37 tiles of them
+static int dw_splits(int M, int N, int K, int act) {
+  const int pairs = sm_count() / 2, nkb = (M + 63) / 64 * dz_parts(act);
+  const int64_t tiles = (int64_t)((N + 255) / 256) * ((K + 127) / 128);
+  if (tiles * 2 > pairs || nkb < 32) return 1;
+  int s = (int)(pairs / tiles);
+  if (s > nkb / 8) s = nkb / 8;
+  return s > 8 ? 8 : s;
+}
+
 struct LinBwdWs {
   bf16 *dz, *tail;  // dz: `parts` matrices [M, ldz]
-  float *part, *dxpart;
+  float *part, *dxpart, *dwpart;
   int64_t ldz, ldt, stride;
   size_t bytes;
 };
@@ -387,6 +411,8 @@ static LinBwdWs lin_bwd_carve(void* ws, int M, int N, int K, int act) {
   const int per = dz_rows_per(M, N);
   w.part = c.take<float>((size_t)((M + per - 1) / per) * N);
   w.dxpart = c.take<float>((lin_part_bytes(lin_shape(M, K, N), M, K) + 3) / 4);
+  const int ks = dw_splits(M, N, K, act);
+  w.dwpart = c.take<float>(ks > 1 ? (size_t)ks * N * K : 0);
   w.bytes = c.used();
   return w;
 }
@@ -536,7 +562,7 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
       parts == 3 ? go(linear_dz_kernel<false, true, 3>) : go(linear_dz_kernel<false, true, 1>);
     prof_end(ps, st);
     JENGA_LAUNCH_CHECK();
-    if (db) {
+    if (db && !dw) {  // with dw its kernel adds them
       const int p2 = prof_begin("linear_db_reduce", st);
       linear_db_reduce_kernel<<<(N + 127) / 128, 128, 0, st>>>(W.part, chunks, N, db, accumulate);
       prof_end(p2, st);
@@ -557,7 +583,11 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
     p.C = K;
     p.m = M;
     p.nkb = (M + 63) / 64;
-    p.ksplit = 1;
+    p.ksplit = dw_splits(M, N, K, act);
+    p.part = W.dwpart;
+    p.db_part = db ? W.part : nullptr;
+    p.db_chunks = chunks;
+    p.db = db;
     p.passes = parts;
     p.n_kept = n_kept;
     p.blk = blk;
@@ -585,6 +615,12 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
     const int64_t t256 = (int64_t)((N + 255) / 256) * ((K + 255) / 256);
     JENGA_TRY((t256 >= sm_count() / 2 ? linear_launch<256, true, true, LIN_GRAD, false>(m, p, "linear_dw", st)
                                       : linear_launch<128, true, true, LIN_GRAD, false>(m, p, "linear_dw", st)));
+    if (p.ksplit > 1) {
+      const int ps = prof_begin("linear_dw_sum", st);
+      linear_dw_sum_kernel<<<dim3((K + 255) / 256, N), 256, 0, st>>>(W.dwpart, p.ksplit, N, K, dw, lddw, accumulate);
+      prof_end(ps, st);
+      JENGA_LAUNCH_CHECK();
+    }
   }
   return JENGA_OK;
 }

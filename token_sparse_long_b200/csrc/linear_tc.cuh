@@ -40,15 +40,16 @@ enum LinMode : int {
 
 // k-blocks (of 64) that a tensor-memory accumulator sums before it is added into fp32
 // registers.  The tensor core truncates when it adds into the accumulator: measured relative
-// loss 4e-6 over 4096 products and 3e-5 over 26240 (1e-4 for all-positive operands), growing
-// with the length.  1024 products at a time keep it near 1e-6 whatever the number of rows.
-constexpr int LT_CHUNK = 16;
+// loss 5e-7 over 512 products, 4e-6 over 4096 and 3e-5 over 26240 (1e-4 for all-positive
+// operands), growing with the length.  512 products at a time keep it at what fp32 sums lose
+// anyway, whatever the number of rows, and the reads hide behind the next products.
+constexpr int LT_CHUNK = 8;
 
 struct LinArgs {
   int R, C, nkb;                  // rows, columns, k-blocks of one pass over the reduction
   int m;                          // host bound on the rows of x (R, or the reduction of LIN_GRAD)
-  int ksplit;                     // LIN_OUT: ranges of k-blocks; above 1 the tiles go to `part`
-  float* part;                    // [ksplit][rows of x][columns of w's side] fp32
+  int ksplit;                     // ranges of k-blocks; above 1 the tiles go to `part`
+  float* part;                    // [ksplit][rows of the result][columns] fp32
   int passes;                     // LIN_GRAD: 3 = A is held in three parts, one pass over the rows each
   const int32_t* n_kept;          // device count of valid blocks of x's rows (nullable)
   int blk;
@@ -62,6 +63,9 @@ struct LinArgs {
   int64_t ldp;
   int out_tma, pre_tma;           // the tensor maps of out / pre are valid
   int accumulate;                 // LIN_GRAD
+  const float* db_part;           // LIN_GRAD: partial column sums of dz [db_chunks][R] (nullable), added
+  int db_chunks;                  //   into db by the first column's tiles while their products run
+  float* db;
   int tail;                       // LIN_GRAD: the last partial k-block comes from the tail copy of x
 };
 
@@ -236,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   const int nkb1 = MODE == LIN_OUT ? p.nkb : (valid + 63) / 64;
   const int nkb_all = nkb1 * (MODE == LIN_GRAD ? p.passes : 1);
   const int ntr = (rows + 255) / 256, ntc = (cols + BN - 1) / BN;
-  const int ksplit = MODE == LIN_OUT ? p.ksplit : 1;
+  const int ksplit = p.ksplit;
   const int ntiles = ntr * ntc * ksplit;
   if (cluster >= ntiles) return;  // uniform over the cluster
   // work tile t: output tile t / ksplit, k-blocks [lo, hi) of range t % ksplit
@@ -329,8 +333,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       int r0, c0, lo, hi;
       tile_at(t, r0, c0, lo, hi);
       for (int kb = lo; ok && kb < hi; ++kb, ++g) {
-        const bool first = MODE == LIN_GRAD ? kb % LT_CHUNK == 0 : kb == lo;
-        const bool last = kb == hi - 1 || (MODE == LIN_GRAD && kb % LT_CHUNK == LT_CHUNK - 1);
+        const bool first = MODE == LIN_GRAD ? (kb - lo) % LT_CHUNK == 0 : kb == lo;
+        const bool last = kb == hi - 1 || (MODE == LIN_GRAD && (kb - lo) % LT_CHUNK == LT_CHUNK - 1);
         const int buf = it & 1;
         if (first && it >= 2 && !__all_sync(0xffffffffu, pair_wait(&acc_empty[buf], ((it >> 1) - 1) & 1))) {
           ok = false;
@@ -570,11 +574,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         ++it;
       } else {
         // LIN_GRAD: add the chunks in fp32 registers, then write the tile
+        if (p.db_part && c0 == 0 && half == 0 && t % ksplit == 0 && r < rows) {
+          float a = 0.f;
+#pragma unroll 4
+          for (int q = 0; q < p.db_chunks; ++q) a += p.db_part[(int64_t)q * p.R + r];
+          p.db[r] = p.accumulate ? p.db[r] + a : a;
+        }
         float acc[BN / 2];
 #pragma unroll
         for (int i = 0; i < BN / 2; ++i) acc[i] = 0.f;
         bool ok = true;
-        for (int kb = 0; kb < hi; kb += LT_CHUNK) {
+        for (int kb = lo; kb < hi; kb += LT_CHUNK) {
           const int buf = it & 1;
           ok = __all_sync(0xffffffffu, pair_wait(&acc_full[buf], (it >> 1) & 1));
           if (!ok) break;
@@ -599,7 +609,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
           const int n = cw + c * 32;
           if (n >= p.C || rw >= rows) continue;
           const float* v = acc + c * 32;
-          if (whole && p.out_tma) {
+          if (ksplit > 1) {
+            if (r < rows) {
+              float* o = p.part + ((int64_t)(t % ksplit) * p.R + r) * p.C + n;
+              if (n + 32 <= p.C && (p.C & 3) == 0) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                  *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (n + i < p.C) o[i] = v[i];
+              }
+            }
+          } else if (whole && p.out_tma) {
             stage_wait();
             uint8_t* tb = stg + (nst & 1) * 4096;
 #pragma unroll
