@@ -47,58 +47,74 @@ constexpr int DROP_ROWS = 4;
 // A thread takes one group of eight columns of DROP_ROWS rows (loads first); row and position are
 // worked out once per row and thread, so that what is left per group is the generator's ten
 // rounds (40 instructions), a comparison, a multiply-add and a select per element -- a flat index
-// with its divisions per group made the kernel compute-bound (135 us against 98 of traffic for
-// 26240 x 4096 with the residual).
+// with its divisions per group made the kernel compute-bound (26240 x 4096 bf16 with the
+// residual through a block list: 138 us; now 104 us, 6.2 TB/s; without the residual 88 us, where
+// the generator bounds it).  Unaligned rows (VEC false) are read and written lane by lane, the
+// bits of a warp's 256 columns passing through shared memory: the words of a group lie there
+// in column order.
 template <typename T, bool VEC, bool RES, int MODE>
-__global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, const T* res, int64_t ldr, T* y,
+__global__ void __launch_bounds__(256, !VEC ? 1 : (sizeof(T) == 2 ? (RES ? 4 : 5) : (RES ? 2 : 3))) dropout_kernel(const T* x, int64_t ldx, const T* res, int64_t ldr, T* y,
                                                       int64_t ldy, DropoutArgs p) {
   constexpr int PER = VEC ? 16 / (int)sizeof(T) : 1, NV = 8 / PER;
+  __shared__ uint4 s_bits[VEC ? 1 : 256];
   const int valid = valid_rows(p.map);
   const int ty = 256 / p.tx, g = blockIdx.x * p.tx + (threadIdx.x & (p.tx - 1));
-  const int c = g * 8;
-  if (g >= p.groups) return;
-  const int step = gridDim.y * ty;  // rows between the unrolled ones
-  for (int64_t r0 = (int64_t)blockIdx.y * ty + threadIdx.x / p.tx; r0 < valid; r0 += (int64_t)step * DROP_ROWS) {
+  const int lane = threadIdx.x & 31;
+  // column of the thread's vector i: eight neighbours, or (VEC false, tx >= 32) every 32nd
+  const int c = VEC ? g * 8 : (g - lane) * 8 + lane;
+  constexpr int CSTEP = VEC ? PER : 32;
+  if ((VEC ? g : g - lane) >= p.groups) return;  // VEC false: the whole warp
+  for (int64_t r0 = (int64_t)blockIdx.y * ty * DROP_ROWS + threadIdx.x / p.tx; r0 < valid;
+       r0 += (int64_t)gridDim.y * ty * DROP_ROWS) {
     RowVec<T, PER> xv[DROP_ROWS][NV], rv[DROP_ROWS][NV];
+    // position = base + row up to the block's last row; the next block is looked up when reached
+    int base = (int)p.row0, next = 0x7fffffff;
+    bool good = true;
+    auto locate = [&](int r) {
+      const int i = (int)fast_div((uint32_t)r, p.blk), b = __ldg(p.map.idx + i);
+      good = b >= 0 && b < p.map.nb && (i == 0 || __ldg(p.map.idx + i - 1) < b);
+      base = good ? (b - i) * p.map.blk : 0;
+      next = (int)min((int64_t)(i + 1) * p.map.blk, (int64_t)0x7fffffff);
+    };
+    if (p.map.idx) locate((int)r0);
 #pragma unroll
     for (int u = 0; u < DROP_ROWS; ++u) {
-      const int64_t r = r0 + (int64_t)u * step;
+      const int64_t r = r0 + u * ty;
       if (r >= valid) continue;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (c + i * PER < p.cols) {
-          if (MODE != DROP_ALL) xv[u][i].load(x + r * ldx + c + i * PER);
-          if (RES) rv[u][i].load(res + r * ldr + c + i * PER);
+        if (c + i * CSTEP < p.cols) {
+          if (MODE != DROP_ALL) xv[u][i].load(x + r * ldx + c + i * CSTEP);
+          if (RES) rv[u][i].load(res + r * ldr + c + i * CSTEP);
         }
       }
     }
 #pragma unroll
     for (int u = 0; u < DROP_ROWS; ++u) {
-      const int64_t r = r0 + (int64_t)u * step;
+      const int64_t r = r0 + u * ty;  // one row per warp where VEC is false
       if (r >= valid) continue;
-      uint32_t w[4] = {0, 0, 0, 0};
-      int64_t pos = p.row0 + r;
-      if (p.map.idx) {
-        const int i = (int)fast_div((uint32_t)r, p.blk), b = __ldg(p.map.idx + i);
-        pos = b < 0 || b >= p.map.nb || (i > 0 && __ldg(p.map.idx + i - 1) >= b)
-                  ? -1
-                  : (int64_t)b * p.map.blk + (r - (int64_t)i * p.map.blk);
-        if (pos < 0) {
-          record_device_error(JENGA_EINTERNAL, SITE_INDEX_RANGE, (unsigned)r);
-          continue;
-        }
+      if (r >= next) locate((int)r);
+      if (!good) {
+        record_device_error(JENGA_EINTERNAL, SITE_INDEX_RANGE, (unsigned)r);
+        continue;
       }
+      uint32_t w[4] = {0, 0, 0, 0};
       if (MODE == DROP_RANDOM) {
         const uint4 bits =
-            philox4x32_10(make_uint4((uint32_t)g, (uint32_t)pos, p.offset[0], p.offset[1]), p.seed[0], p.seed[1]);
+            philox4x32_10(make_uint4((uint32_t)g, (uint32_t)(base + (int)r), p.offset[0], p.offset[1]), p.seed[0], p.seed[1]);
         w[0] = bits.x;
         w[1] = bits.y;
         w[2] = bits.z;
         w[3] = bits.w;
+        if (!VEC) {
+          __syncwarp();  // the row before is done
+          s_bits[threadIdx.x] = bits;
+          __syncwarp();
+        }
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        if (c + i * PER < p.cols) {
+        if (c + i * CSTEP < p.cols) {
           float f[PER], q[PER];
           if (MODE != DROP_ALL) xv[u][i].get(f);
           if (RES) rv[u][i].get(q);
@@ -106,11 +122,16 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, c
           for (int e = 0; e < PER; ++e) {
             const int k = i * PER + e;
             // the 16-bit number against T: in the high half the low half does not matter
-            const bool keep = MODE == DROP_NONE || (MODE == DROP_RANDOM && ((k & 1) ? w[k >> 1] : w[k >> 1] << 16) >= p.threshold);
-            if (MODE == DROP_ALL) f[e] = RES ? q[e] : 0.f;
-            else f[e] = RES ? (keep ? fmaf(f[e], p.scale, q[e]) : q[e]) : (keep ? f[e] * p.scale : 0.f);
+            uint32_t n = (k & 1) ? w[k >> 1] : w[k >> 1] << 16;
+            if (!VEC && MODE == DROP_RANDOM)
+              n = (uint32_t)reinterpret_cast<const uint16_t*>(s_bits + (threadIdx.x - lane))[i * 32 + lane] << 16;
+            const bool keep = MODE == DROP_NONE || (MODE == DROP_RANDOM && n >= p.threshold);
+            if (MODE == DROP_ALL)
+              f[e] = RES ? q[e] : 0.f;
+            else
+              f[e] = RES ? (keep ? fmaf(f[e], p.scale, q[e]) : q[e]) : (keep ? f[e] * p.scale : 0.f);
           }
-          RowVec<T, PER>::store(y + r * ldy + c + i * PER, f);
+          RowVec<T, PER>::store(y + r * ldy + c + i * CSTEP, f);
         }
       }
     }
@@ -170,7 +191,7 @@ extern "C" jenga_status jenga_dropout(const void* x, int64_t ldx, const void* re
   a.offset[1] = (uint32_t)(offset >> 32);
   a.blk = make_fastdiv((uint32_t)blk);
   a.tx = 256;
-  while (a.tx > 1 && a.tx / 2 >= a.groups) a.tx /= 2;
+  while (a.tx > (vec ? 1 : 32) && a.tx / 2 >= a.groups) a.tx /= 2;
   const int strips = (a.groups + a.tx - 1) / a.tx, ty = 256 / a.tx;
   // one step of DROP_ROWS rows a thread, or a loop beyond the grid's limit
   const int64_t want = ((int64_t)rows + (int64_t)ty * DROP_ROWS - 1) / ((int64_t)ty * DROP_ROWS);

@@ -87,7 +87,8 @@ __device__ __forceinline__ bool ln_claim(LnRing& st, int64_t row, int r, int s, 
 }
 
 // Barrier of a row group (a warp, or else the CTA) that also agrees on `ok`: a warp that timed out
-// takes all with it.
+// takes all with it.  (Barrier 0 only: a barrier number in a register would reserve all 16 for
+// the CTA, and four such CTAs are all that an SM then holds.)
 __device__ __forceinline__ bool group_agree(bool ok, int gw) {
   if (gw > 1) return __syncthreads_and(ok);
   ok = __all_sync(0xffffffffu, ok);
@@ -418,75 +419,104 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 320 ? 2 : 1)
 }
 
 // ------------------------------------------------------------------ unaligned rows
-// The same sums with element-wise loads straight into registers, for rows that are not whole
-// 16-byte vectors (odd widths, odd pitches, unaligned bases): a thread holds NV elements, 32 gw
-// apart.  gw == 1: four rows per CTA, one per warp; wider rows: the CTA is the row group.
-template <typename T, int NV>
-__global__ void __launch_bounds__(NV <= 16 ? 1024 : 128) layernorm_fwd_kernel(const T* x, int64_t ldx, RowMap map, int h, int gw,
-                                                             const void* gamma, const void* beta, int wbf16,
-                                                             float eps, T* y, int64_t ldy, float* mean_out,
-                                                             float* rstd_out) {
-  constexpr int VEC = 1;
-  __shared__ float s_red[2][32];
+// Element-wise loads, for rows that are not whole 16-byte vectors (odd widths, odd pitches,
+// unaligned bases): a thread holds NV elements, 32 gw apart.  Forward and backward keep gamma
+// (and beta, or the sums) in registers over the rows of a persistent group and load the next
+// row's elements before this row is reduced.
+template <typename T, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 128 ? 5 : (MAXT <= 256 ? 2 : 1))
+    layernorm_fwd_kernel(const T* x, int64_t ldx, RowMap map, int h, int gw, const void* gamma, const void* beta,
+                         int wbf16, float eps, T* y, int64_t ldy, float* mean_out, float* rstd_out) {
+  __shared__ float2 s_red[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gwarp = gw == 1 ? 0 : warp;
-  const int r = gw == 1 ? blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
-  if (r >= valid_rows(map)) return;  // uniform over the row group
-  const int64_t row = sequence_row(map, r);
-  if (row < 0) {
-    if (lane == 0 && gwarp == 0) record_device_error(JENGA_EINTERNAL, SITE_INDEX_RANGE, (unsigned)r);
-    return;
-  }
-  const T* xr = x + row * ldx;
-  const int nvec = h / VEC, step = gw * 32, t0 = gwarp * 32 + lane;
-  RowVec<T, VEC> v[NV];
-  float s = 0.f;
+  const int groups = (blockDim.x >> 5) / gw, grp = warp / gw, gwarp = warp - grp * gw;
+  const int step = gw * 32, t0 = gwarp * 32 + lane;
+  const int valid = valid_rows(map);
+  const int G = gridDim.x * groups;
+  const int64_t r0 = blockIdx.x * groups + grp;
+  int p2 = 1;  // lane l combines warp l mod p2's sums
+  while (p2 < gw) p2 *= 2;
+  const int lw = lane & (p2 - 1);
+  auto held = [&](int w) {  // elements of a row that warp w of the group holds
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) n += max(0, min(32, h - (w * 32 + i * step)));
+    return (float)n;
+  };
+  const float inv_h = 1.f / (float)h, cnt = held(gwarp), inv_cnt = cnt > 0.f ? 1.f / cnt : 0.f;
+  const float ocnt = lw < gw ? held(lw) : 0.f, inv_ocnt = ocnt > 0.f ? 1.f / ocnt : 0.f;
+  float ga[NV], be[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    v[i].zero();
-    if (t0 + i * step < nvec) v[i].load(xr + (int64_t)(t0 + i * step) * VEC);
+    ga[i] = be[i] = 0.f;
+    if (t0 + i * step < h) {
+      load_params<1>(gamma, wbf16, t0 + i * step, 1.f, &ga[i]);
+      load_params<1>(beta, wbf16, t0 + i * step, 0.f, &be[i]);
+    }
   }
+  RowVec<T, 1> nxt[NV];
+  auto fetch = [&](int64_t r) {
+    if (r >= valid) return false;
+    const int64_t row = sequence_row(map, (int)r);
+    if (row < 0) {
+      if (t0 == 0) record_device_error(JENGA_EINTERNAL, SITE_INDEX_RANGE, (unsigned)r);
+      return false;
+    }
+    const T* p = x + row * ldx + t0;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float f[VEC];
-    v[i].get(f);
+    for (int i = 0; i < NV; ++i)
+      if (t0 + i * step < h) nxt[i].load(p + i * step);
+    return true;
+  };
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) s += f[e];
-  }
-  const float inv_h = 1.f / (float)h;
-  const float mean = group_sum(s, s_red[0], gwarp, gw) * inv_h;
-  float q = 0.f;
+  for (int i = 0; i < NV; ++i) nxt[i].zero();
+  bool live = fetch(r0);
+  int par = 0;
+  for (int64_t r = r0; r < valid; r += G) {
+    float f[NV], sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (t0 + i * step < nvec) {
-      float f[VEC];
-      v[i].get(f);
+    for (int i = 0; i < NV; ++i) {
+      nxt[i].get(&f[i]);
+      if (t0 + i * step < h) sum += f[i];
+    }
+    const bool now = live;  // the same for the whole group
+    live = fetch(r + G);
+    if (!now) continue;
+    sum = warp_sum(sum);
+    const float wm = sum * inv_cnt;
+    float m2 = 0.f;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = f[e] - mean;
-        q = fmaf(d, d, q);
+    for (int i = 0; i < NV; ++i) {
+      f[i] -= wm;
+      if (t0 + i * step < h) m2 = fmaf(f[i], f[i], m2);
+    }
+    m2 = warp_sum(m2);
+    float mean = sum * inv_h;
+    if (gw > 1) {
+      if (lane == 0) s_red[par][warp] = make_float2(sum, m2);
+      __syncthreads();  // the CTA is the row group
+      const float2 v = lw < gw ? s_red[par][lw] : make_float2(0.f, 0.f);
+      mean = v.x;
+      for (int o = p2 >> 1; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+      mean *= inv_h;
+      const float d = fmaf(v.x, inv_ocnt, -mean);
+      m2 = fmaf(ocnt * d, d, v.y);
+      for (int o = p2 >> 1; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+      par ^= 1;
+    }
+    const float rstd = 1.f / sqrtf(m2 * inv_h + eps);
+    if (t0 == 0) {
+      if (mean_out) mean_out[r] = mean;
+      if (rstd_out) rstd_out[r] = rstd;
+    }
+    const float off = (wm - mean) * rstd;
+    T* yr = y + r * ldy + t0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (t0 + i * step < h) {
+        const float o = fmaf(fmaf(f[i], rstd, off), ga[i], be[i]);
+        RowVec<T, 1>::store(yr + i * step, &o);
       }
-    }
-  }
-  const float var = group_sum(q, s_red[1], gwarp, gw) * inv_h;
-  const float rstd = 1.f / sqrtf(var + eps);
-  if (t0 == 0) {
-    if (mean_out) mean_out[r] = mean;
-    if (rstd_out) rstd_out[r] = rstd;
-  }
-  T* yr = y + (int64_t)r * ldy;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t)(t0 + i * step) * VEC;
-    if (t0 + i * step < nvec) {
-      float f[VEC], ga[VEC], be[VEC];
-      v[i].get(f);
-      load_params<VEC>(gamma, wbf16, c, 1.f, ga);
-      load_params<VEC>(beta, wbf16, c, 0.f, be);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) f[e] = fmaf((f[e] - mean) * rstd, ga[e], be[e]);
-      RowVec<T, VEC>::store(yr + c, f);
-    }
   }
 }
 
@@ -544,6 +574,9 @@ __global__ void __launch_bounds__(MAXT)
       }
     }
   };
+  int p2 = 1;  // lane l adds warp l mod p2's sums
+  while (p2 < gw) p2 *= 2;
+  const int lw = lane & (p2 - 1);
   const float inv_h = 1.f / (float)h;
   BwdRow<T, NV> cur, nxt;
   const int r0 = blockIdx.x * groups + grp;
@@ -577,11 +610,11 @@ __global__ void __launch_bounds__(MAXT)
           s_red[par][1][warp] = s2;
         }
         __syncthreads();
-        s1 = 0.f;
-        s2 = 0.f;
-        for (int i = 0; i < gw; ++i) {
-          s1 += s_red[par][0][grp * gw + i];
-          s2 += s_red[par][1][grp * gw + i];
+        s1 = lw < gw ? s_red[par][0][lw] : 0.f;
+        s2 = lw < gw ? s_red[par][1][lw] : 0.f;
+        for (int o = p2 >> 1; o > 0; o >>= 1) {
+          s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+          s2 += __shfl_xor_sync(0xffffffffu, s2, o);
         }
         par ^= 1;
       }
@@ -753,20 +786,24 @@ static cudaError_t ln_fwd_ring(const LnShape& s, const LnFwdCall& c, cudaStream_
                                   : go(layernorm_fwd_ring_kernel<T, NV, false, MAXT>);
   return e;
 }
-template <typename T, int NV>
-static cudaError_t ln_fwd_one(const LnFwdCall& c, cudaStream_t st) {
-  const int gw = (c.h + 32 * NV - 1) / (32 * NV);
-  layernorm_fwd_kernel<T, NV><<<gw == 1 ? (c.map.rows + 3) / 4 : c.map.rows, gw == 1 ? 128 : gw * 32, 0, st>>>(
+template <typename T, int NV, int MAXT>
+static cudaError_t ln_fwd_one(const LnFwdCall& c, int gw, cudaStream_t st) {
+  const int groups = gw == 1 ? 4 : 1, warps = gw * groups;
+  const int per_sm = warps <= 4 ? 20 / warps : (warps <= 8 ? 2 : 1);
+  const int want = (c.map.rows + groups - 1) / groups, cap = per_sm * sm_count();
+  layernorm_fwd_kernel<T, NV, MAXT><<<want < cap ? want : cap, warps * 32, 0, st>>>(
       (const T*)c.x, c.ldx, c.map, c.h, gw, c.gamma, c.beta, c.wbf16, c.eps, (T*)c.y, c.ldy, c.mean, c.rstd);
   return cudaSuccess;
 }
 template <typename T>
 static cudaError_t ln_fwd(bool aligned, const LnFwdCall& c, cudaStream_t st) {
   if (!aligned) {
-    if (c.h <= 64) return ln_fwd_one<T, 2>(c, st);
-    if (c.h <= 256) return ln_fwd_one<T, 8>(c, st);
-    if (c.h <= 1024) return ln_fwd_one<T, 32>(c, st);
-    return ln_fwd_one<T, 16>(c, st);
+    const int gw = c.h <= 512 ? 1 : (c.h + 511) / 512;  // 16 elements a thread
+    if (c.h <= 128) return ln_fwd_one<T, 4, 128>(c, 1, st);
+    if (gw <= 4) return ln_fwd_one<T, 16, 128>(c, gw, st);
+    if (gw <= 8) return ln_fwd_one<T, 16, 256>(c, gw, st);
+    if (gw <= 16) return ln_fwd_one<T, 16, 512>(c, gw, st);
+    return ln_fwd_one<T, 16, 1024>(c, gw, st);
   }
   const LnShape s = ln_fwd_shape(c.map.rows, c.h, sizeof(T));
   if (s.nv == 1) return ln_fwd_ring<T, 1, 128>(s, c, st);  // a warp holds the row: four rows a CTA

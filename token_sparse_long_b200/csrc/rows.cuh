@@ -136,21 +136,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the `n` warps of a row group (one warp, or else the CTA); `slot` holds a float per
-// warp.  Two alternating slots need one barrier a sum: a warp writes a slot again only after
-// every warp has passed the other slot's barrier, that is after every warp has read this one.
-// (Barrier 0 only: a barrier number in a register reserves all 16 for the CTA, and four such
-// CTAs are all that an SM then holds.)
-__device__ __forceinline__ float group_sum(float v, float* slot, int warp, int n) {
-  v = warp_sum(v);
-  if (n == 1) return v;
-  if ((threadIdx.x & 31) == 0) slot[warp] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < n; ++i) s += slot[i];
-  return s;
-}
-
 __device__ __forceinline__ bool aligned16_dev(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Bounded wait like mbar_wait, reading the timer and the budget only every 256 polls (each poll
