@@ -457,6 +457,50 @@ def test_dropout_positions_segments_and_backward(J):
     assert torch.equal(J.jenga_dropout(pit, 0.3, 5, 6), full)
 
 
+# ------------------------------------------------------------------ large matrices
+def test_offsets_beyond_32_bits(J):
+    # every matrix below holds more than 2^31 elements: the last rows against the same rows alone
+    bf = torch.bfloat16
+    if torch.cuda.get_device_properties(0).total_memory < 60 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    h, rows = 8192, (1 << 18) + 700
+    x = torch.randn(1024, h, device="cuda").to(bf).repeat(rows // 1024 + 1, 1)[:rows]
+    ga = randn(1, h, dt=bf)
+    t = rows - 333
+    y, mean, rstd = J.jenga_layernorm_fwd(x, ga)
+    want = J.jenga_layernorm_fwd(x[t:].clone(), ga)
+    assert torch.equal(y[t:], want[0]) and torch.equal(mean[t:], want[1])
+    dx = J.jenga_layernorm_bwd(y, x, mean, rstd, ga, weight_grads=False)[0]
+    assert torch.equal(dx[t:], J.jenga_layernorm_bwd(y[t:].clone(), x[t:].clone(), mean[t:].clone(), rstd[t:].clone(), ga,
+                                                     weight_grads=False)[0])
+    del dx
+    J.jenga_dropout(x, 0.3, 5, 6, out=y)
+    assert torch.equal(y[t:], J.jenga_dropout(x[t:].clone(), 0.3, 5, 6, row0=t))
+    del x, y
+    M, N, K = 200100, 11008, 64
+    x, w = randn(2, M, K, dt=bf), randn(3, N, K, dt=bf, scale=0.2)
+    y, pre = J.jenga_linear_fwd(x, w, act="relu", save_pre=True)
+    v = M - 300
+    ry, rz = od.linear_fwd(f64(x[v:]), f64(w), None, "relu")
+    S = np.abs(f64(x[v:])) @ np.abs(f64(w)).T
+    close(y[v:], ry, 2 * (K + 2) * U * S + RB * np.abs(ry) * 1.001 + 1e-30)
+    close(pre[v:], rz, 2 * (K + 2) * U * S + RB * np.abs(rz) * 1.001 + 1e-30)
+    dx, _, _ = J.jenga_linear_bwd(y, x, w, act="relu", pre=pre, need=("dx",))
+    dy, z = f64(y[v:]), f64(pre[v:])
+    rx = (dy * (z > 0)) @ f64(w)
+    close(dx[v:], rx, 2 * (N + 2) * U * (np.abs(dy) @ np.abs(f64(w))) + RB * np.abs(rx) * 1.001 + 1e-30)
+    J.jenga_check_device_status()
+
+
+def test_dropout_more_rows_than_one_grid(J):
+    rows, cols = 4 * 65535 + 300, 2048  # the grid holds 65535 steps of four rows of this width
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    y = J.jenga_dropout(x, 0.25, 9, 3)
+    for s in (0, 4 * 65535 - 100, rows - 200):
+        assert torch.equal(y[s:s + 200], J.jenga_dropout(x[s:s + 200], 0.25, 9, 3, row0=s))
+    assert abs(float((y != 0).float().mean()) - 0.75) < 1e-3
+
+
 # ------------------------------------------------------------------ streams, graphs, repeated calls
 def _all_ops(J, t):
     y, mean, rstd = J.jenga_layernorm_fwd(t["x"], t["ga"], t["be"])
@@ -522,6 +566,8 @@ def test_binding_refuses_what_the_kernels_cannot_read(J):
                  lambda: J.jenga_dropout(x, 0.5, 0, idx=torch.tensor([0], dtype=torch.int32, device="cuda"), blk=4)):
         with pytest.raises(E + (KeyError,)):
             call()
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    assert J.jenga_layernorm_fwd(x, idx=none, blk=8)[0].shape == (0, 64)
     empty = J.jenga_linear_fwd(x[:0], w)[0]
     assert empty.shape == (0, 16)
     _, dw, db = J.jenga_linear_bwd(empty, x[:0], w)

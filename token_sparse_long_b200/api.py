@@ -431,8 +431,10 @@ def _vec(t, name, n, dtype=None):
 def _rows_arg(idx, n_kept, blk, n_kept_max, rows):
     """Rows of a call: n_kept_max blocks with a block list, else `rows`."""
     for t, name in ((idx, "idx"), (n_kept, "n_kept")):
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < 1):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
             raise ValueError(f"{name}: contiguous int32 required")
+    if n_kept is not None and n_kept.numel() != 1:
+        raise ValueError(f"n_kept: one count required, got {tuple(n_kept.shape)}")
     if idx is None:
         return rows
     n = idx.numel() if n_kept_max is None else int(n_kept_max)
@@ -471,8 +473,8 @@ def jenga_layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, idx=None, n_kept=Non
             rstd = x.new_empty(rows, dtype=torch.float32)
         else:
             _vec(rstd, "rstd", rows, torch.float32)
-        check(load().jenga_layernorm_fwd(x.data_ptr(), ldx, S, h, _ptr(idx), _ptr(n_kept), blk, rows, _ptr(gamma),
-                                         _ptr(beta), _dt(w) if w is not None else F32, eps, dt, y.data_ptr(), ldy,
+        check(load().jenga_layernorm_fwd(x.data_ptr(), ldx, S, h, _ptr(idx), _ptr(n_kept), int(blk), rows, _ptr(gamma),
+                                         _ptr(beta), _dt(w) if w is not None else F32, float(eps), dt, y.data_ptr(), ldy,
                                          mean.data_ptr(), rstd.data_ptr(), s))
     finally:
         _end(guard)
@@ -516,7 +518,7 @@ def jenga_layernorm_bwd(dy, x, mean, rstd, gamma=None, idx=None, n_kept=None, bl
         lib = load()
         if ws is None and (dgamma is not None or dbeta is not None):
             ws = x.new_empty(lib.jenga_layernorm_bwd_workspace_bytes(rows, h), dtype=torch.uint8)
-        check(lib.jenga_layernorm_bwd(dy.data_ptr(), ldy, x.data_ptr(), ldx, S, h, _ptr(idx), _ptr(n_kept), blk, rows,
+        check(lib.jenga_layernorm_bwd(dy.data_ptr(), ldy, x.data_ptr(), ldx, S, h, _ptr(idx), _ptr(n_kept), int(blk), rows,
                                       mean.data_ptr(), rstd.data_ptr(), _ptr(gamma),
                                       _dt(gamma) if gamma is not None else F32, _ptr(dres), ldr, dt, dx.data_ptr(),
                                       ldd, _ptr(dgamma), _ptr(dbeta), 1 if accumulate else 0, _ptr(ws),
@@ -557,7 +559,7 @@ def jenga_linear_fwd(x, w, bias=None, act="none", residual=None, n_kept=None, bl
             ws = x.new_empty(nws, dtype=torch.uint8)
         check(lib.jenga_linear_fwd(x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(bias),
                                    _dt(bias) if bias is not None else F32, ACTIVATIONS[act], _ptr(residual), ldr, M, N,
-                                   K, _ptr(n_kept), blk, y.data_ptr(), ldy, _ptr(pre), ldp, _ptr(ws),
+                                   K, _ptr(n_kept), int(blk), y.data_ptr(), ldy, _ptr(pre), ldp, _ptr(ws),
                                    ws.numel() if ws is not None else 0, s))
     finally:
         _end(guard)
@@ -609,7 +611,7 @@ def jenga_linear_bwd(dy, x, w, act="none", pre=None, n_kept=None, blk=1, need=("
         if ws is None:
             ws = x.new_empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, a), dtype=torch.uint8)
         check(lib.jenga_linear_bwd(dy.data_ptr(), ldy, x.data_ptr(), ldx, w.data_ptr(), ldw, a, _ptr(pre), ldp, M, N, K,
-                                   _ptr(n_kept), blk, _ptr(dx), ldd, _ptr(dw), lddw, _ptr(db), 1 if accumulate else 0,
+                                   _ptr(n_kept), int(blk), _ptr(dx), ldd, _ptr(dw), lddw, _ptr(db), 1 if accumulate else 0,
                                    ws.data_ptr(), ws.numel(), s))
     finally:
         _end(guard)
@@ -635,8 +637,8 @@ def jenga_dropout(x, p, seed, offset=0, residual=None, idx=None, n_kept=None, bl
         y = x.new_empty((rows, cols)) if out is None else out
         ldy = cols if out is None else _mat(y, "out", cols, rows, x.dtype)
         m64 = (1 << 64) - 1
-        check(load().jenga_dropout(x.data_ptr(), ldx, _ptr(residual), ldr, rows, cols, _ptr(idx), _ptr(n_kept), blk,
-                                   row0, p, seed & m64, offset & m64, dt, y.data_ptr(), ldy, s))
+        check(load().jenga_dropout(x.data_ptr(), ldx, _ptr(residual), ldr, rows, cols, _ptr(idx), _ptr(n_kept), int(blk),
+                                   int(row0), float(p), int(seed) & m64, int(offset) & m64, dt, y.data_ptr(), ldy, s))
     finally:
         _end(guard)
     return y

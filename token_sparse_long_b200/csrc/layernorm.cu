@@ -710,8 +710,6 @@ struct LnShape {
   int vec, nv, gw, groups, ctas, stages;
   size_t smem;
 };
-constexpr int LN_CTAS_PER_SM = 8;  // most of the backward (sizes the partial sums)
-
 // Aligned forward.  bf16 is bound by instruction issue next to memory: 32 columns a thread spread
 // the per-row steps (barrier, shuffles, copies) over more of them, at 16 warps an SM (26240 x
 // 4096: 78 us against 92 with 16 columns and 24 warps; 5120 wide: 94 against 122).  fp32 moves
@@ -730,7 +728,7 @@ static LnShape ln_fwd_shape(int rows, int h, int es) {
   s.stages = room / (per_stage * per_sm);  // 3 rows of 64 KB at the least
   s.stages = s.stages > LN_MAX_STAGES ? LN_MAX_STAGES : s.stages;
   s.smem = (size_t)s.stages * per_stage;
-  const int want = (rows + s.groups - 1) / s.groups, cap = per_sm * sm_count();
+  const int want = (rows - 1) / s.groups + 1, cap = per_sm * sm_count();
   s.ctas = want < cap ? want : cap;
   return s;
 }
@@ -757,7 +755,7 @@ static LnShape ln_bwd_shape(int rows, int h, int es, bool aligned, int mats) {
   }
   const size_t sums = s.groups > 1 ? (size_t)s.groups * 2 * h * sizeof(float) : 0;
   if (s.smem < sums) s.smem = sums;
-  const int want = (rows + s.groups - 1) / s.groups, cap = per_sm * sm_count();
+  const int want = (rows - 1) / s.groups + 1, cap = per_sm * sm_count();
   s.ctas = want < cap ? want : cap;
   return s;
 }
@@ -790,7 +788,7 @@ template <typename T, int NV, int MAXT>
 static cudaError_t ln_fwd_one(const LnFwdCall& c, int gw, cudaStream_t st) {
   const int groups = gw == 1 ? 4 : 1, warps = gw * groups;
   const int per_sm = warps <= 4 ? 20 / warps : (warps <= 8 ? 2 : 1);
-  const int want = (c.map.rows + groups - 1) / groups, cap = per_sm * sm_count();
+  const int want = (c.map.rows - 1) / groups + 1, cap = per_sm * sm_count();
   layernorm_fwd_kernel<T, NV, MAXT><<<want < cap ? want : cap, warps * 32, 0, st>>>(
       (const T*)c.x, c.ldx, c.map, c.h, gw, c.gamma, c.beta, c.wbf16, c.eps, (T*)c.y, c.ldy, c.mean, c.rstd);
   return cudaSuccess;
@@ -934,8 +932,14 @@ extern "C" jenga_status jenga_layernorm_fwd(const void* x, int64_t ldx, int S, i
 
 extern "C" size_t jenga_layernorm_bwd_workspace_bytes(int rows, int h) {
   if (rows < 1 || h < 1 || h > LN_MAX_H) return 0;
-  const int cap = LN_CTAS_PER_SM * sm_count();
-  return (size_t)(rows < cap ? rows : cap) * 2 * h * sizeof(float) + 256;
+  int ctas = 0;  // the most of the types, alignments and residual forms
+  for (int es = 2; es <= 4; es += 2)
+    for (int mats = 2; mats <= 3; ++mats)
+      for (int aligned = 0; aligned <= (h % (16 / es) == 0); ++aligned) {
+        const int n = ln_bwd_shape(rows, h, es, aligned, mats).ctas;
+        ctas = n > ctas ? n : ctas;
+      }
+  return (size_t)ctas * 2 * h * sizeof(float) + 256;
 }
 
 extern "C" jenga_status jenga_layernorm_bwd(const void* dy, int64_t ldy, const void* x, int64_t ldx, int S, int h,
