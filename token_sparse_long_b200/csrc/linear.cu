@@ -19,45 +19,36 @@ namespace jenga {
 // lane and four rows a step per warp (loads first: two matrices, one pass, bound by memory); the
 // eight warps' sums are added in order, part[chunk][N].  Rows from the valid count up to the
 // next multiple of 64 are written as zeros (the product over the rows reads whole 64-row
-// blocks).  VEC: rows of dy and pre are 16-byte aligned.
+// blocks).  VEC: rows of dy and pre are whole 16-byte vectors.
 template <bool VEC, bool WRITE, int PARTS>
 __global__ void __launch_bounds__(256)
     linear_dz_kernel(const bf16* __restrict__ dy, int64_t ldy, const bf16* __restrict__ pre, int64_t ldp, int act,
                      int M, int N, const int32_t* n_kept, int blk, int rows_per, bf16* __restrict__ dz, int64_t ldz,
                      int64_t part_stride, float* __restrict__ part) {
-  constexpr int STEP = 4;
+  constexpr int STEP = 4, PER = VEC ? 8 : 1, NV = 8 / PER;  // unaligned: every 32nd column, element by element
+  constexpr int CSTEP = VEC ? 8 : 32;
   __shared__ float s_sum[8][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int valid = valid_rows(RowMap{nullptr, n_kept, blk, 0, M});
-  const int c = blockIdx.x * 256 + lane * 8;
+  const int cl = VEC ? lane * 8 : lane, c = blockIdx.x * 256 + cl;  // first column in the strip and overall
   const int r_lo = blockIdx.y * rows_per;
   const int r_hi = min(min((valid + 63) / 64 * 64, M), r_lo + rows_per);
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
   if (c < N) {
-    const bool whole = VEC && c + 8 <= N;
     for (int r0 = r_lo + warp; r0 < r_hi; r0 += 8 * STEP) {
-      RowVec<bf16, 8> a[STEP], b[STEP];
+      RowVec<bf16, PER> a[STEP][NV], b[STEP][NV];
 #pragma unroll
       for (int u = 0; u < STEP; ++u) {
         const int r = r0 + u * 8;
-        a[u].zero();
-        b[u].zero();
-        if (r < r_hi && r < valid) {
-          if (whole) {
-            a[u].load(dy + (int64_t)r * ldy + c);
-            if (act != JENGA_ACT_NONE) b[u].load(pre + (int64_t)r * ldp + c);
-          } else {
-            bf16* av = reinterpret_cast<bf16*>(&a[u].r);
-            bf16* bv = reinterpret_cast<bf16*>(&b[u].r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (c + e < N) {
-                av[e] = dy[(int64_t)r * ldy + c + e];
-                if (act != JENGA_ACT_NONE) bv[e] = pre[(int64_t)r * ldp + c + e];
-              }
-            }
+        for (int i = 0; i < NV; ++i) {
+          a[u][i].zero();
+          b[u][i].zero();
+          if (r < r_hi && r < valid && c + i * CSTEP < N) {
+            a[u][i].load(dy + (int64_t)r * ldy + c + i * CSTEP);
+            if (act != JENGA_ACT_NONE) b[u][i].load(pre + (int64_t)r * ldp + c + i * CSTEP);
           }
         }
       }
@@ -66,8 +57,11 @@ __global__ void __launch_bounds__(256)
         const int r = r0 + u * 8;
         if (r >= r_hi) break;
         float d[8], z[8];
-        a[u].get(d);
-        b[u].get(z);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          a[u][i].get(d + i * PER);
+          b[u][i].get(z + i * PER);
+        }
         if (act == JENGA_ACT_RELU) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) d[e] = z[e] > 0.f ? d[e] : 0.f;
@@ -77,14 +71,17 @@ __global__ void __launch_bounds__(256)
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += d[e];
-        if (WRITE) {  // the pitch is a multiple of 8: a vector may reach into the padding
+        if (WRITE) {
           bf16* o = dz + (int64_t)r * ldz + c;
-          RowVec<bf16, 8>::store(o, d);
 #pragma unroll
-          for (int q = 1; q < PARTS; ++q) {
+          for (int q = 0; q < PARTS; ++q) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] -= __bfloat162float(__float2bfloat16_rn(d[e]));
-            RowVec<bf16, 8>::store(o + q * part_stride, d);
+            for (int i = 0; i < NV; ++i)
+              if (c + i * CSTEP < N) RowVec<bf16, PER>::store(o + q * part_stride + i * CSTEP, d + i * PER);
+            if (q + 1 < PARTS) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) d[e] -= __bfloat162float(__float2bfloat16_rn(d[e]));
+            }
           }
         }
       }
@@ -92,7 +89,9 @@ __global__ void __launch_bounds__(256)
   }
   if (!part) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s_sum[warp][lane * 8 + e] = sum[e];
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < PER; ++e) s_sum[warp][cl + i * CSTEP + e] = sum[i * PER + e];
   __syncthreads();
   const int col = blockIdx.x * 256 + threadIdx.x;
   if (col < N) {
@@ -547,7 +546,7 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
   const int per = dz_rows_per(M, N), chunks = (M + per - 1) / per;
   if (!direct || db) {
     float* part = db ? W.part : nullptr;
-    const bool vec = lin_operand_ok(dy, ldy) && (!pre || lin_operand_ok(pre, ldp));
+    const bool vec = N % 8 == 0 && lin_operand_ok(dy, ldy) && (!pre || lin_operand_ok(pre, ldp));
     const dim3 grid((N + 255) / 256, chunks);
     auto go = [&](auto kernel) {
       kernel<<<grid, 256, 0, st>>>((const bf16*)dy, ldy, (const bf16*)pre, ldp, act, M, N, n_kept, blk, per, W.dz, W.ldz,
@@ -555,7 +554,7 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
     };
     const int ps = prof_begin("linear_dz", st);
     if (direct)
-      go(linear_dz_kernel<true, false, 1>);
+      vec ? go(linear_dz_kernel<true, false, 1>) : go(linear_dz_kernel<false, false, 1>);
     else if (vec)
       parts == 3 ? go(linear_dz_kernel<true, true, 3>) : go(linear_dz_kernel<true, true, 1>);
     else
