@@ -21,6 +21,7 @@ movement   permutation-free gather and in-place scatter-add
 lm_loss    causal-LM cross-entropy over the vocabulary and its hidden-state gradient
 mlp_blocks MLP-block elimination criterion (|SiLU(gate) * up| mass per block) and index composition
 layer      retained-token Llama decoder layer forward and backward (+ segmented)
+dense      layer norm, linear layer, dropout (Philox4x32-10) and their gradients
 predictor  block-score predictor MLP (mean pool -> Linear -> GELU -> Linear)
 rank       rank agreement statistics (Spearman, Kendall tau-b, top-k recall)
 
