@@ -397,12 +397,13 @@ JENGA_API jenga_status jenga_lm_loss_segmented(const void* hidden, const void* w
  * residual) -> scatter, and back.
  *
  * Rows.  A call covers `rows` (M) compact rows, a host bound.  n_kept (device int32, nullable)
- * counts the valid blocks of blk rows: rows at and past *n_kept * blk are neither read nor
- * written, and add nothing to a reduction; an *n_kept outside [0, rows / blk] is recorded
- * (JENGA_EINTERNAL) and the call treats no row as valid.  With idx (device int32, ascending block list) compact row r is
- * sequence row idx[r / blk] * blk + r % blk; an entry that is out of range or not
- * above the entry before it is recorded and its rows are skipped.  rows must be whole blocks when idx or n_kept is given;
- * blk is 1 or more and otherwise unused without them.
+ * counts the valid blocks of blk rows: rows at and past *n_kept * blk are not written, add
+ * nothing to a reduction and may hold anything (NaN included); an *n_kept outside
+ * [0, rows / blk] is recorded (JENGA_EINTERNAL) and the call treats no row as valid.  With idx
+ * (device int32, ascending block list) compact row r is sequence row
+ * idx[r / blk] * blk + r % blk; an entry that is out of range or not above the entry before it
+ * is recorded and its rows are skipped (a block listed twice leaves its rows undefined).  rows
+ * must be whole blocks when idx or n_kept is given; blk is 1 or more and otherwise unused.
  * Pitches (ld*) are in elements.  An output may be the same matrix as an input (same pointer
  * and pitch) where stated, and must not overlap one otherwise (JENGA_EINVAL).
  * rows = 0 is a call without work (overwritten gradients become zeros). */

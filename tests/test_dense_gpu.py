@@ -220,6 +220,77 @@ def test_layernorm_bwd(J, rows, h, dt, res):
     assert torch.equal(dx3, dx) and none_g is None and none_b is None
 
 
+@pytest.mark.parametrize("rows,h,dt", [(5000, 4096, torch.bfloat16), (3200, 5120, torch.bfloat16),
+                                       (4000, 2048, torch.float32), (20000, 264, torch.bfloat16)])
+def test_layernorm_many_rows_a_group(J, rows, h, dt):
+    """More rows a group than the ring has stages, through a list with a bad entry in the middle."""
+    blk = 40
+    S = rows + 5 * blk
+    x = randn(h, S, h, dt=dt, shift=1.0)
+    ga, be = randn(1, h, dt=dt, shift=1.0), randn(2, h, dt=dt)
+    lst, rowsel = kept(S, blk, rows // blk, 3)
+    bad = rows // blk // 2
+    ok = torch.ones(rows, dtype=torch.bool, device="cuda")
+    want = J.jenga_layernorm_fwd(x[rowsel].contiguous(), ga, be)
+    ry, rm, rr = od.layernorm_fwd(f64(x[rowsel]), f64(ga), f64(be))
+    close(want[0], ry, ln_tol(f64(x[rowsel]), rm, rr, f64(ga), ry, dt) + 4 * U * np.abs(f64(be)))
+    for spoil in (False, True):
+        if spoil:
+            lst[bad] = S
+            ok[bad * blk:(bad + 2) * blk] = False  # the entry, and the next one, which is not above it
+        y, mean, rstd = J.jenga_layernorm_fwd(x, ga, be, idx=lst, blk=blk, out=torch.full((rows, h), 7.0, dtype=dt, device="cuda"))
+        assert torch.equal(y[ok], want[0][ok]) and torch.equal(mean[ok], want[1][ok])
+        assert (y[~ok] == 7.0).all()
+        mean[~ok], rstd[~ok] = 0.0, 1.0
+        dy = randn(4, rows, h, dt=dt)
+        dx, dg, db = J.jenga_layernorm_bwd(dy, x, mean, rstd, ga, idx=lst, blk=blk)
+        if spoil:
+            with pytest.raises(J._lib.JengaError):
+                J.jenga_check_device_status()
+        else:
+            J.jenga_check_device_status()
+        k = ok.cpu().numpy()
+        X, D = f64(x[rowsel])[k], f64(dy)[k]
+        m, r = f64(mean)[k], f64(rstd)[k]
+        wx, wg, wb = od.layernorm_bwd(D, X, m, r, f64(ga))
+        n = np.abs((X - m[:, None]) * r[:, None])
+        g = np.abs(D * f64(ga))
+        q = h / 32 + 60
+        c1, c2 = g.mean(1, keepdims=True), (g * n).mean(1, keepdims=True)
+        tol = r[:, None] * (6 * U * g + (q + 6) * U * c1 + n * (q + 12) * U * c2) + (HALF[dt] + 4 * U) * np.abs(wx)
+        close(dx[rowsel][ok], wx, tol * 1.01 + 1e-30)
+        close(dg, wg, (rows + 10) * U * (np.abs(D) * n).sum(0) + 1e-30)
+        close(db, wb, (rows + 10) * U * np.abs(D).sum(0) + 1e-30)
+
+
+def test_layernorm_unaligned_bases_and_in_place_gradients(J):
+    bf = torch.bfloat16
+    x, dy = randn(1, 90, 520, dt=bf), randn(2, 90, 520, dt=bf)
+    ga, be = randn(3, 520, dt=bf, shift=1.0), randn(4, 520, dt=bf)
+    y, mean, rstd = J.jenga_layernorm_fwd(x, ga, be)
+    wx, wg, wb = J.jenga_layernorm_bwd(dy, x, mean, rstd, ga)
+
+    def off(t):  # the same values one element into a buffer
+        b = torch.full((t.numel() + 1,), NAN, dtype=t.dtype, device="cuda")
+        b[1:] = t.reshape(-1)
+        return b[1:].view(t.shape)
+
+    y2, m2, r2 = J.jenga_layernorm_fwd(off(x), off(ga), be)
+    close(y2, f64(y), 2 * RB * np.abs(f64(y)) + 1e-6)
+    x2, g2, b2 = J.jenga_layernorm_bwd(off(dy), x, mean, rstd, off(ga))
+    close(x2, f64(wx), 2 * RB * np.abs(f64(wx)) + 1e-6)
+    close(g2, f64(wg), 1e-5 * np.abs(f64(wg)) + 1e-4)
+    for which in ("dy", "x"):
+        a, b = dy.clone(), x.clone()
+        out = a if which == "dy" else b
+        J.jenga_layernorm_bwd(a, b, mean, rstd, ga, dx=out)
+        assert torch.equal(out, wx)
+    nx = J.jenga_layernorm_bwd(dy, x, mean, rstd)[0]
+    rx, _, _ = od.layernorm_bwd(f64(dy), f64(x), f64(mean), f64(rstd))
+    close(nx, rx, RB * np.abs(rx) * 1.01 + 1e-4 * f64(rstd)[:, None])
+    J.jenga_check_device_status()
+
+
 # ------------------------------------------------------------------ linear
 ACTS = ["none", "relu", "gelu", "silu"]
 
@@ -289,6 +360,46 @@ def test_linear_fwd_device_count(J, M):
         J.jenga_check_device_status()
         assert torch.equal(out[:v], want[:v]) and torch.equal(pre[:v], wpre[:v])
         assert (out[v:] == 7.0).all() and (pre[v:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 700, 512), (2, 300, 4096), (20, 520, 4096), (96, 300, 4096), (300, 260, 2048),
+                                   (3000, 3, 70), (1500, 1100, 64)])
+def test_linear_fwd_every_shape_in_place_and_counted(J, M, N, K):
+    """Each route (rows of w, swapped, split reductions, wide) with y = residual and a device count."""
+    x, w, b, res = lin_case(M, N, K)
+    want, wpre = J.jenga_linear_fwd(x, w, b, act="silu", residual=res, save_pre=True)
+    ry, rz = od.linear_fwd(f64(x), f64(w), f64(b), "silu", f64(res))
+    S = np.abs(f64(x)) @ np.abs(f64(w)).T + np.abs(f64(b))
+    close(want, ry, 1.13 * 2 * (K + 2) * U * S + act_err(rz, "silu") + (4 * U + RB * 1.001) * np.abs(ry)
+          + 2 * U * np.abs(f64(res)))
+    y = res.clone()
+    J.jenga_linear_fwd(x, w, b, act="silu", residual=y, out=y)
+    assert torch.equal(y, want)
+    n = M // 2
+    x2, y2 = pitched(x, -K % 8 + 8), res.clone()
+    x2[n:] = NAN
+    J.jenga_linear_fwd(x2, w, b, act="silu", residual=y2, out=y2, n_kept=torch.tensor([n], dtype=torch.int32, device="cuda"))
+    assert torch.equal(y2[:n], want[:n]) and torch.equal(y2[n:], res[n:])
+    J.jenga_check_device_status()
+
+
+def test_linear_bwd_split_sum_with_a_device_count(J):
+    M, N, K = 2560, 300, 136  # dw's reduction is split over idle SM pairs
+    x, w, _, dy = lin_case(M, N, K)
+    pre = randn(9, M, N, dt=torch.bfloat16)
+    for v in (0, 65, 1300, M):
+        x2, dy2 = x.clone(), dy.clone()
+        x2[v:], dy2[v:] = NAN, NAN
+        dw = pitched(torch.ones(N, K, device="cuda"), 4)
+        db = torch.ones(N, device="cuda")
+        J.jenga_linear_bwd(dy2, x2, w, act="relu", pre=pre, n_kept=torch.tensor([v], dtype=torch.int32, device="cuda"),
+                           need=("dw", "db"), dw=dw, db=db, accumulate=True)
+        X, W, D, Z = f64(x[:v]), f64(w), f64(dy[:v]), f64(pre[:v])
+        _, rw, rb, dz = od.linear_bwd(D, X, W, "relu", Z)
+        _, tw, tb = bwd_tols(X, W, D, dz, slope_err(Z, "relu"), v, "relu")
+        close(dw, rw + 1, tw + 2 * U * (np.abs(rw) + 1))
+        close(db, rb + 1, tb + 2 * U * (np.abs(rb) + 1))
+    J.jenga_check_device_status()
 
 
 def test_linear_fwd_extremes(J):
@@ -426,8 +537,9 @@ def test_dropout(J, rows, cols, dt):
             assert ((f64(y) != 0) == (want != 0)).all()
 
 
-def test_dropout_positions_segments_and_backward(J):
-    S, blk, n, h = 1024, 64, 9, 264
+@pytest.mark.parametrize("h", [264, 265, 20])
+def test_dropout_positions_segments_and_backward(J, h):
+    S, blk, n = 1024, 64, 9
     x = randn(1, S, h, dt=torch.bfloat16)
     full = J.jenga_dropout(x, 0.3, 5, 6)
     idx, rows = kept(S, blk, n, 2)
