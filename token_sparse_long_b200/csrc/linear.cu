@@ -271,7 +271,7 @@ static jenga_status linear_launch(const LinMats& m, const LinArgs& p, const char
   const int pairs = sm_count() / 2;
   const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
   const int ps = prof_begin(name, st);
-  kernel<<<grid, LT_THREADS, L::TOTAL, st>>>(m.a, m.a2, m.a3, m.b, m.tail, m.out, m.pre, p);
+  kernel<<<grid, lin_threads<BN>, L::TOTAL, st>>>(m.a, m.a2, m.a3, m.b, m.tail, m.out, m.pre, p);
   prof_end(ps, st);
   JENGA_LAUNCH_CHECK();
   return JENGA_OK;

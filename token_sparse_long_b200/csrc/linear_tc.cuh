@@ -16,11 +16,14 @@
 // A = w or w^T, and x or dz the narrow one -- so that the weights, which are all the traffic,
 // spread over every SM; and a product with few tiles splits its reduction (ksplit) into fp32
 // partial products that linear_finish adds in order.
-// 320 threads per CTA:
+// 320 threads per CTA (352 for tiles up to 128 wide):
 //   warp 0      TMA producer (both CTAs; completion counted on the leader's full barrier)
 //   warp 1      allocates tensor memory; in the leader one lane issues the MMAs and commits
 //               (multicast to both CTAs' barriers)
 //   warps 2..9  epilogue: two warps per TMEM lane quarter, half of the columns each
+//   warp 10     in the leader, the MMAs of every other k-block of a narrow tile, into an
+//               accumulator of its own that the epilogue adds: a warp issues an MMA only
+//               every 116 clocks or so, which is more than a tile of 128 columns needs
 // Persistent: one cluster per SM pair walks the tiles in bands of 8 row tiles (row tile
 // fastest), so that a wave's operands stay within L2.
 #pragma once
@@ -30,7 +33,6 @@
 
 namespace jenga {
 
-constexpr int LT_THREADS = 320;
 constexpr int LT_BAND = 8;
 
 enum LinMode : int {
@@ -68,6 +70,11 @@ struct LinArgs {
   float* db;
   int tail;                       // LIN_GRAD: the last partial k-block comes from the tail copy of x
 };
+
+template <int BN>
+constexpr int lin_mma_warps = BN <= 128 ? 2 : 1;
+template <int BN>
+constexpr int lin_threads = BN <= 128 ? 352 : 320;
 
 template <int BN, bool SWAP>
 struct LinSmem {
@@ -214,13 +221,13 @@ __global__ void __launch_bounds__(128) linear_finish_kernel(LinArgs p, int N) {
 }
 
 template <int BN, bool AMN, bool BMN, int MODE, bool SWAP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                      const __grid_constant__ CUtensorMap tmA3, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmTail, const __grid_constant__ CUtensorMap tmOut,
                      const __grid_constant__ CUtensorMap tmPre, LinArgs p) {
   using L = LinSmem<BN, SWAP>;
   static_assert(!(BMN && BN < 128), "an MN-major B half is at least one 64-wide box");
-  constexpr int ST = L::STAGES;
+  constexpr int ST = L::STAGES, MW = lin_mma_warps<BN>, ACC = MW * BN;  // columns of an accumulator set
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -263,12 +270,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_full[b], MW);
       mbar_init(&acc_empty[b], 16);
     }
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc_pair(tmem_holder, 2 * BN);
+  if (warp == 1) tmem_alloc_pair(tmem_holder, 2 * ACC);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
@@ -323,47 +330,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
     if (rank == 0)
       for (int i = g > ST ? g - ST : 0; i < g; ++i)
         if (!pair_wait(&full[i % ST], (i / ST) & 1)) break;
-  } else if (warp == 1 && rank == 0) {
-    // ---------------- MMA issuer (leader)
+  } else if ((warp == 1 || warp == 10) && rank == 0) {
+    // ---------------- MMA issuers (leader): warp mw takes k-blocks mw, mw + MW, ... of each unit (a
+    // tile, or a chunk of LIN_GRAD)
+    const int mw = warp == 1 ? 0 : 1;
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
                            ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
     bool ok = true;
-    int g = 0, it = 0;
+    int g = 0, it = 0;  // k-blocks before the tile; units so far
     for (int t = cluster; ok && t < ntiles; t += nclusters) {
       int r0, c0, lo, hi;
       tile_at(t, r0, c0, lo, hi);
-      for (int kb = lo; ok && kb < hi; ++kb, ++g) {
-        const bool first = MODE == LIN_GRAD ? (kb - lo) % LT_CHUNK == 0 : kb == lo;
-        const bool last = kb == hi - 1 || (MODE == LIN_GRAD && (kb - lo) % LT_CHUNK == LT_CHUNK - 1);
+      for (int u0 = lo; ok && u0 < hi; u0 += LT_CHUNK) {
+        const int u1 = MODE == LIN_GRAD ? min(u0 + LT_CHUNK, hi) : hi;
         const int buf = it & 1;
-        if (first && it >= 2 && !__all_sync(0xffffffffu, pair_wait(&acc_empty[buf], ((it >> 1) - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        const int s = g % ST;
-        if (!__all_sync(0xffffffffu, pair_wait(&full[s], (g / ST) & 1))) {
+        if (it >= 2 && !__all_sync(0xffffffffu, pair_wait(&acc_empty[buf], ((it >> 1) - 1) & 1))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t acc = tmem + buf * BN;
-        const uint32_t sa = smem_u32(smem + s * L::STAGE_BYTES);
-        const uint32_t sb = sa + L::A_BYTES;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t da = AMN ? umma_desc_mn_sw128(sa + k * 2048, 8192) : umma_desc_k_sw128(sa + k * 32);
-            const uint64_t db = BMN ? umma_desc_mn_sw128(sb + k * 2048, 8192) : umma_desc_k_sw128(sb + k * 32);
-            umma_pair(acc, da, db, idesc, (!first || k > 0) ? 1u : 0u);
+        const uint32_t acc = tmem + buf * ACC + mw * BN;
+        for (int kb = u0 + mw; kb < u1; kb += MW) {
+          const int gk = g + kb - lo, s = gk % ST;
+          if (!__all_sync(0xffffffffu, pair_wait(&full[s], (gk / ST) & 1))) {
+            ok = false;
+            break;
           }
-          umma_commit_pair(&empty[s]);
-          if (last) umma_commit_pair(&acc_full[buf]);
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + s * L::STAGE_BYTES);
+          const uint32_t sb = sa + L::A_BYTES;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t da = AMN ? umma_desc_mn_sw128(sa + k * 2048, 8192) : umma_desc_k_sw128(sa + k * 32);
+              const uint64_t db = BMN ? umma_desc_mn_sw128(sb + k * 2048, 8192) : umma_desc_k_sw128(sb + k * 32);
+              umma_pair(acc, da, db, idesc, (kb > u0 + mw || k > 0) ? 1u : 0u);
+            }
+            umma_commit_pair(&empty[s]);
+          }
+          __syncwarp();
         }
+        if (ok && elect_one()) umma_commit_pair(&acc_full[buf]);  // without MMAs of its own: at once
         __syncwarp();
-        if (last) ++it;
+        ++it;
+        if (MODE == LIN_OUT) break;
       }
+      g += hi - lo;
     }
-  } else if (warp >= 2) {
+  } else if (warp >= 2 && warp < 10) {
     // ---------------- epilogue
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stg = smem + L::STG_OFF + (warp - 2) * 2 * 4096;
@@ -427,8 +441,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
             const int m0 = cw + cc * 16;
             uint32_t raw[16];
             __syncwarp();  // the load below is collective
-            tmem_ld16_nowait(lane_base + buf * BN + cc * 16, raw);
-            tmem_wait_ld();
+            tmem_ld16_nowait(lane_base + buf * ACC + cc * 16, raw);
+            if (MW == 2 && hi - lo > 1) {  // the second warp's k-blocks
+              uint32_t more[16];
+              tmem_ld16_nowait(lane_base + buf * ACC + BN + cc * 16, more);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) + __uint_as_float(more[i]));
+            } else {
+              tmem_wait_ld();
+            }
             if (cc == BN / 32 - 1) {
               tc_fence_before();
               __syncwarp();
@@ -473,9 +495,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
         for (int cc = 0; cc < BN / 128; ++cc) {
           const int n = cw + cc * 64;
           uint32_t raw[64];
-          tmem_ld32_nowait(lane_base + buf * BN + cc * 64, raw);
-          tmem_ld32_nowait(lane_base + buf * BN + cc * 64 + 32, raw + 32);
-          tmem_wait_ld();
+          tmem_ld32_nowait(lane_base + buf * ACC + cc * 64, raw);
+          tmem_ld32_nowait(lane_base + buf * ACC + cc * 64 + 32, raw + 32);
+          if (MW == 2 && hi - lo > 1) {  // the second warp's k-blocks
+            uint32_t more[64];
+            tmem_ld32_nowait(lane_base + buf * ACC + BN + cc * 64, more);
+            tmem_ld32_nowait(lane_base + buf * ACC + BN + cc * 64 + 32, more + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 64; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) + __uint_as_float(more[i]));
+          } else {
+            tmem_wait_ld();
+          }
           if (cc == BN / 128 - 1) {  // the accumulator is read: release it
             tc_fence_before();
             __syncwarp();
@@ -592,10 +623,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
 #pragma unroll
           for (int c = 0; c < BN / 64; ++c) {
             uint32_t raw[32];
-            tmem_ld32_nowait(lane_base + buf * BN + c * 32, raw);
+            tmem_ld32_nowait(lane_base + buf * ACC + c * 32, raw);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[c * 32 + i] += __uint_as_float(raw[i]);
+            if (MW == 2 && hi - kb > 1) {  // the second warp's k-blocks
+              tmem_ld32_nowait(lane_base + buf * ACC + BN + c * 32, raw);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[c * 32 + i] += __uint_as_float(raw[i]);
+            }
           }
           tc_fence_before();
           __syncwarp();
@@ -655,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LT_THREADS, 1)
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 2 * BN);
+    tmem_dealloc_pair(tmem, 2 * ACC);
   }
 }
 
