@@ -284,8 +284,10 @@ static bool out_map(CUtensorMap* map, const void* base, int rows, int cols, int6
 
 // Shape of a forward or dx product [M, N] over `red`: operands swapped (and the narrow side's
 // tile), tile width, ranges of the reduction.  Costs in k-blocks of a 256-wide tile (530 clocks
-// measured; a 128-wide tile's take 390 and a narrow swapped one's about as long, since the issue
-// of the four MMAs does not shrink).  A further tile of a cluster costs its epilogue's start;
+// measured; a narrower tile's take 215 to 250 with operands in L2, but about 400 when they come
+// from HBM, which few rows make the rule: over M 16 to 4096 and seven pairs of N and K, 0.75 was
+// never more than 3% behind 0.5 or 0.6 but at M 512 4096->1024, and up to 13% ahead of them).
+// A further tile of a cluster costs its epilogue's start;
 // a split adds the pass over the partial products: a launch, and 0.8 MB a k-block of time.
 struct LinShape {
   bool swap;
@@ -353,6 +355,8 @@ static jenga_status lin_out(const LinShape& s, const void* x, int64_t ldx, const
     if (s.ksplit == 1) {
       p.out_tma = out_map(&m.out, p.out, M, N, p.ldo);
       p.pre_tma = out_map(&m.pre, p.pre, M, N, p.ldp);
+    } else {
+      p.out_tma = N % 4 == 0 && make_tmap_f32(&m.out, p.part, (uint64_t)s.ksplit * M, N, N, 32) == JENGA_OK;
     }
     JENGA_TRY((s.bn == 256 ? linear_launch<256, false, WMN, LIN_OUT, false>(m, p, name, st)
                            : linear_launch<128, false, WMN, LIN_OUT, false>(m, p, name, st)));
@@ -610,7 +614,10 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
       JENGA_LAUNCH_CHECK();
       JENGA_TRY(make_tmap_bf16(&m.tail, W.tail, 64, K, W.ldt, 64));
     }
-    p.out_tma = is16(dw) && lddw % 4 == 0 && make_tmap_f32(&m.out, dw, N, K, lddw, 32) == JENGA_OK;
+    if (p.ksplit > 1)
+      p.out_tma = K % 4 == 0 && make_tmap_f32(&m.out, p.part, (uint64_t)p.ksplit * N, K, K, 32) == JENGA_OK;
+    else
+      p.out_tma = is16(dw) && lddw % 4 == 0 && make_tmap_f32(&m.out, dw, N, K, lddw, 32) == JENGA_OK;
     const int64_t t256 = (int64_t)((N + 255) / 256) * ((K + 255) / 256);
     JENGA_TRY((t256 >= sm_count() / 2 ? linear_launch<256, true, true, LIN_GRAD, false>(m, p, "linear_dw", st)
                                       : linear_launch<128, true, true, LIN_GRAD, false>(m, p, "linear_dw", st)));

@@ -275,12 +275,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
     }
     fence_barrier_init();
   }
+  // The pair's barriers are ready after this cluster barrier.  Tensor memory is allocated
+  // meanwhile: the warps that read it wait for that here, and the leader's MMAs for the first
+  // arrivals on acc_empty, which come from both CTAs; the loads start 700 clocks sooner.
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   if (warp == 1) tmem_alloc_pair(tmem_holder, 2 * ACC);
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync_all();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  uint32_t tmem = 0;
+  if (warp != 0) {
+    tc_fence_before();
+    asm volatile("bar.sync 2, %0;" ::"n"(lin_threads<BN> - 32) : "memory");
+    tc_fence_after();
+    tmem = *tmem_holder;
+  }
 
   if (warp == 0) {
     // ---------------- TMA producer (the warp stays converged and elects a lane to issue: from a
@@ -344,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
       for (int u0 = lo; ok && u0 < hi; u0 += LT_CHUNK) {
         const int u1 = MODE == LIN_GRAD ? min(u0 + LT_CHUNK, hi) : hi;
         const int buf = it & 1;
-        if (it >= 2 && !__all_sync(0xffffffffu, pair_wait(&acc_empty[buf], ((it >> 1) - 1) & 1))) {
+        if (!__all_sync(0xffffffffu, pair_wait(&acc_empty[buf], (it >> 1) & 1))) {
           ok = false;
           break;
         }
@@ -384,6 +392,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + half * (BN / 2);
     const uint32_t empty_leader[2] = {map_rank(smem_u32(&acc_empty[0]), 0), map_rank(smem_u32(&acc_empty[1]), 0)};
     float* s_bias = reinterpret_cast<float*>(smem + L::BIAS_OFF);
+    if (lane == 0) {  // both accumulators are free at first: each CTA's is allocated
+      mbar_arrive_cluster(empty_leader[0]);
+      mbar_arrive_cluster(empty_leader[1]);
+    }
     bool alive = true;
     int nst = 0;
     auto stage_wait = [&] {  // the store that last read staging tile nst & 1 is done
@@ -514,6 +526,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
           }
           if (n >= p.C || rw >= rows) continue;
           const bool full_cols = n + 64 <= p.C;
+          if (ksplit > 1 && whole && p.out_tma) {  // the map's rows: ksplit blocks of p.m
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (n + 32 * h >= p.C) continue;
+              stage_wait();
+              uint8_t* tb = stg + (nst & 1) * 4096;
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4*>(tb + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                    make_uint4(raw[32 * h + 4 * q], raw[32 * h + 4 * q + 1], raw[32 * h + 4 * q + 2], raw[32 * h + 4 * q + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) tma_store_2d(&tmOut, tb, n + 32 * h, t % ksplit * p.m + rw);
+              stage_done();
+            }
+            continue;
+          }
           if (ksplit > 1) {
             if (r < rows) {
               float* o = p.part + ((int64_t)(t % ksplit) * p.m + r) * p.C + n;
@@ -646,20 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
           const int n = cw + c * 32;
           if (n >= p.C || rw >= rows) continue;
           const float* v = acc + c * 32;
-          if (ksplit > 1) {
-            if (r < rows) {
-              float* o = p.part + ((int64_t)(t % ksplit) * p.R + r) * p.C + n;
-              if (n + 32 <= p.C && (p.C & 3) == 0) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                  *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (n + i < p.C) o[i] = v[i];
-              }
-            }
-          } else if (whole && p.out_tma) {
+          if (whole && p.out_tma) {
             stage_wait();
             uint8_t* tb = stg + (nst & 1) * 4096;
 #pragma unroll
@@ -669,12 +685,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              if (p.accumulate)
+              if (ksplit > 1)  // the map's rows: ksplit blocks of p.R
+                tma_store_2d(&tmOut, tb, n, t % ksplit * p.R + rw);
+              else if (p.accumulate)
                 tma_reduce_add_2d(&tmOut, tb, n, rw);
               else
                 tma_store_2d(&tmOut, tb, n, rw);
             }
             stage_done();
+          } else if (r < rows && ksplit > 1) {
+            float* o = p.part + ((int64_t)(t % ksplit) * p.R + r) * p.C + n;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (n + i < p.C) o[i] = v[i];
           } else if (r < rows) {
             float* o = reinterpret_cast<float*>(p.out) + (int64_t)r * p.ldo + n;
 #pragma unroll
