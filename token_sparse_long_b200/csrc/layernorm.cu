@@ -25,18 +25,7 @@ namespace jenga {
 // (group g of G takes rows g, g + G, ...), so what belongs to a column stays in registers.
 // Arithmetic is on fp32 pairs.
 
-// fp32 pairs of one 16-byte vector
-template <typename T>
-__device__ __forceinline__ void vec_pairs(const uint4& r, uint64_t* f) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = f2pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-  } else {
-    f[0] = f2pack(__uint_as_float(w[0]), __uint_as_float(w[1]));
-    f[1] = f2pack(__uint_as_float(w[2]), __uint_as_float(w[3]));
-  }
-}
+// fp32 pairs as one 16-byte vector
 template <typename T>
 __device__ __forceinline__ uint4 pairs_vec(const uint64_t* f) {
   uint32_t w[4];
@@ -58,12 +47,6 @@ __device__ __forceinline__ uint4 pairs_vec(const uint64_t* f) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ float pair_sum(uint64_t v) {
-  float a, b;
-  f2unpack(v, a, b);
-  return a + b;
-}
-
 constexpr int LN_MAX_STAGES = 8;
 
 // Row group state of the ring: per stage a barrier and the sequence row (-1: a bad list

@@ -149,9 +149,11 @@ __global__ void __launch_bounds__(256) linear_tail_kernel(const bf16* __restrict
 constexpr int GV_BATCH = 64;
 constexpr int GV_MAX_STAGES = 64;
 template <int MT, int NV>
-__global__ void __launch_bounds__(288)
+__global__ void __launch_bounds__(288, 1)
     linear_rows_kernel(const bf16* __restrict__ w, int64_t ldw, const bf16* __restrict__ x, int64_t ldx, int N, int K,
                        int G, int stages, LinArgs p) {
+  constexpr int NB = NV < 8 ? NV : 8;  // vectors of a row in flight to registers
+  static_assert(GV_BATCH * MT <= 256, "a thread finishes one value of a batch");
   extern __shared__ __align__(128) uint8_t s_w[];
   __shared__ uint64_t s_full[GV_MAX_STAGES], s_empty[GV_MAX_STAGES];
   __shared__ float s_part[2][GV_BATCH][MT][8];
@@ -159,17 +161,16 @@ __global__ void __launch_bounds__(288)
   const int valid = valid_rows(RowMap{nullptr, p.n_kept, p.blk, 0, p.m});
   const int lo = (int)((int64_t)N * blockIdx.x / gridDim.x), hi = (int)((int64_t)N * (blockIdx.x + 1) / gridDim.x);
   const uint32_t row_bytes = (uint32_t)K * 2;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < stages; ++i) {
+  if (valid == 0) return;
+  if (warp == 8) {
+    // ---------------- producer: its copies start before the others have come this far
+    for (int i = lane; i < stages; i += 32) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], G);
     }
     fence_barrier_init();
-  }
-  __syncthreads();
-  if (valid == 0) return;
-  if (warp == 8) {
-    // ---------------- producer
+    __syncwarp();
+    asm volatile("bar.arrive 2, 288;" ::: "memory");
     int s = 0, ph = 1;  // the first lap finds every stage free
     for (int n = lo; n < hi; ++n) {
       if (!__all_sync(0xffffffffu, poll_wait(&s_empty[s], ph, SITE_LINEAR))) return;
@@ -188,45 +189,58 @@ __global__ void __launch_bounds__(288)
   // ---------------- eight warps of dot products
   const int groups = 8 / G, grp = warp / G, gwarp = warp - grp * G;
   const int nvec = K / 8, v0 = gwarp * 32 + lane, step = G * 32;
-  float xf[MT][NV][8];
+  uint64_t xf[MT][NV][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      RowVec<bf16, 8> v;
-      v.zero();
-      if (m < valid && v0 + i * step < nvec) v.load(x + (int64_t)m * ldx + (int64_t)(v0 + i * step) * 8);
-      v.get(xf[m][i]);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (m < valid && v0 + i * step < nvec)
+        v = *reinterpret_cast<const uint4*>(x + (int64_t)m * ldx + (int64_t)(v0 + i * step) * 8);
+      vec_pairs<bf16>(v, xf[m][i]);
     }
+  asm volatile("bar.sync 2, 288;" ::: "memory");  // the barriers are ready
   bool ok = true;
   int s = grp, ph = 0;  // the group's stage (stages >= groups)
   for (int b0 = lo, bi = 0; b0 < hi; b0 += GV_BATCH, bi ^= 1) {
     const int b1 = min(b0 + GV_BATCH, hi);
+    // the value that this thread finishes below, and its bias
+    const int fm = threadIdx.x / (b1 - b0), fq = threadIdx.x - fm * (b1 - b0);
+    float bias = 0.f;
+    if (fm < MT) load_params<1>(p.bias, p.bias_bf16, b0 + fq, 0.f, &bias);
     for (int n = b0 + grp; n < b1; n += groups) {
       ok = __all_sync(0xffffffffu, poll_wait(&s_full[s], ph, SITE_LINEAR));
       if (!ok) break;
       const uint8_t* row = s_w + (size_t)s * row_bytes + v0 * 16;
-      float acc[MT][2];
+      uint64_t acc[MT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = 0.f;
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (v0 + i * step < nvec) {
-          RowVec<bf16, 8> v;
-          float f[8];
-          v.r = *reinterpret_cast<const uint4*>(row + i * step * 16);
-          v.get(f);
+        for (int e = 0; e < 4; ++e) acc[m][e] = 0;
+#pragma unroll
+      for (int i0 = 0; i0 < NV; i0 += NB) {
+        uint4 raw[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (v0 + (i0 + i) * step < nvec) raw[i] = *reinterpret_cast<const uint4*>(row + (i0 + i) * step * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          uint64_t f[4];
+          vec_pairs<bf16>(raw[i], f);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[m][e & 1] = fmaf(f[e], xf[m][i][e], acc[m][e & 1]);
+            for (int e = 0; e < 4; ++e) acc[m][e] = ffma2(f[e], xf[m][i0 + i][e], acc[m][e]);
         }
       }
       __syncwarp();  // every lane has read the row
       if (lane == 0) mbar_arrive(&s_empty[s]);
       float t[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) t[m] = acc[m][0] + acc[m][1];
+      for (int m = 0; m < MT; ++m)
+        t[m] = pair_sum(fadd2(fadd2(acc[m][0], acc[m][1]), fadd2(acc[m][2], acc[m][3])));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -242,17 +256,10 @@ __global__ void __launch_bounds__(288)
       }
     }
     if (!bar_and(ok, 1, 256)) return;  // a warp that timed out takes the others with it
-    for (int i = threadIdx.x; i < (b1 - b0) * MT; i += 256) {
-      const int m = i / (b1 - b0), q = i - m * (b1 - b0);
-      if (m >= valid) continue;
+    if (fm < MT && fm < valid) {
       float z = 0.f;
-      for (int k = 0; k < G; ++k) z += s_part[bi][q][m][k];
-      if (p.bias) {
-        float b;
-        load_params<1>(p.bias, p.bias_bf16, b0 + q, 0.f, &b);
-        z += b;
-      }
-      lin_finish(p, m, b0 + q, z);
+      for (int k = 0; k < G; ++k) z += s_part[bi][fq][fm][k];
+      lin_finish(p, fm, b0 + fq, z + bias);
     }
   }
 }

@@ -92,6 +92,24 @@ struct RowVec<float, 1> {
   static __device__ __forceinline__ void store(float* p, const float* f) { *p = f[0]; }
 };
 
+// fp32 pairs of one 16-byte vector
+template <typename T>
+__device__ __forceinline__ void vec_pairs(const uint4& r, uint64_t* f) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  } else {
+    f[0] = f2pack(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    f[1] = f2pack(__uint_as_float(w[2]), __uint_as_float(w[3]));
+  }
+}
+__device__ __forceinline__ float pair_sum(uint64_t v) {
+  float a, b;
+  f2unpack(v, a, b);
+  return a + b;
+}
+
 // N consecutive parameters (N = 1, 4 or 8) of type F32 or BF16; `fill` without a tensor.
 // N > 1 needs a 16-byte aligned tensor and a column that is a multiple of N.
 template <int N>
