@@ -139,13 +139,16 @@ __global__ void __launch_bounds__(256) linear_tail_kernel(const bf16* __restrict
 // Forward for one or two rows of x: the weights are the whole traffic, read once.  Each CTA takes
 // a consecutive share of w's rows and streams them through a ring of whole rows in shared memory
 // (bulk copies by a warp of their own, up to 190 KB in flight an SM whatever the others do).
-// A group of G warps takes a row: it holds its slice of x as fp32 in registers (NV vectors of
-// eight a thread), so a weight is read from shared memory once and used MT times, and with G = 1
-// eight rows are reduced side by side (all eight warps on one row: 400 clocks a row).  The
-// sums of GV_BATCH rows at a time meet in shared memory, where the epilogue runs.  fp32
-// products and sums.  One row of 4096 into 32000: 52 us, 5.1 TB/s; into 11008: 23 us (the tensor
-// core kernel with its second launch: 24, and 18 against 13 us into 4096); at four rows the
-// products bound it (78 us) and the tensor cores win.
+// A group of G warps takes a row: it holds its slice of x as fp32 pairs in registers (NV vectors
+// of eight a thread), so a weight is read from shared memory once and used MT times, and with
+// G = 1 eight rows are reduced side by side (all eight warps on one row: 400 clocks a row).  A
+// warp needs about as long for a row as memory for eight, so its loads are issued eight at a
+// time and vectors past the row's end are zeros, not branches (23 -> 21 us).  The sums of GV_BATCH
+// rows at a time meet in shared memory, where the epilogue runs.  fp32 products and sums.  One
+// row of 4096 into 32000: 46 us, 5.7 TB/s; into 11008: 21 us and into 4096: 10.6 us, of which
+// 5.5 are the launch and the way to the first row (the tensor core kernel with its second launch:
+// 27 and 17 us).  Four rows with G = 4 were slower than the tensor cores (63 against 50 us into
+// 32000, 54 against 31 for 5120 into 13824).
 constexpr int GV_BATCH = 64;
 constexpr int GV_MAX_STAGES = 64;
 template <int MT, int NV>
@@ -241,14 +244,22 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
         t[m] = pair_sum(fadd2(fadd2(acc[m][0], acc[m][1]), fadd2(acc[m][2], acc[m][3])));
+      // lanes halve the rows of x among them as they add: after log2(MT) exchanges lanes
+      // 32/MT m .. of row m hold one sum each
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
+      for (int o = 16, c = MT / 2; o > 0; o >>= 1, c /= 2) {
+        if (c > 0) {
+          const bool up = lane & o;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) t[m] += __shfl_xor_sync(0xffffffffu, t[m], o);
-      if (lane == 0) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) s_part[bi][n - b0][m][gwarp] = t[m];
+          for (int m = 0; m < c; ++m) {
+            const float give = up ? t[m] : t[m + c], keep = up ? t[m + c] : t[m];
+            t[m] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        } else {
+          t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
+        }
       }
+      if (lane % (32 / MT) == 0) s_part[bi][n - b0][lane / (32 / MT)][gwarp] = t[0];
       s += groups;
       if (s >= stages) {
         s -= stages;
