@@ -393,11 +393,11 @@ static jenga_status lin_out(const LinShape& s, const void* x, int64_t ldx, const
 
 static bool lin_operand_ok(const void* p, int64_t ld) { return is16(p) && ld % 8 == 0; }
 
-static int dz_rows_per(int M, int N) {  // rows per chunk of linear_dz: about four CTAs an SM, whole 64-row blocks
+static int dz_rows_per(int M, int N) {  // rows per chunk of linear_dz: about four CTAs an SM, whole steps of 32
   const int strips = (N + 255) / 256;
   int chunks = (4 * sm_count() + strips - 1) / strips;
   int per = (M + chunks - 1) / chunks;
-  per = (per + 63) / 64 * 64;
+  per = (per + 31) / 32 * 32;
   return per;
 }
 
@@ -423,8 +423,8 @@ struct LinBwdWs {
 };
 static LinBwdWs lin_bwd_carve(void* ws, int M, int N, int K, int act) {
   LinBwdWs w;
-  w.ldz = (N + 7) / 8 * 8;
-  w.ldt = (K + 7) / 8 * 8;
+  w.ldz = (N + 63) / 64 * 64;  // whole 128-byte lines: a box of other rows takes TMA 1.2 to 1.4 times as long
+  w.ldt = (K + 63) / 64 * 64;
   w.stride = (int64_t)M * w.ldz;
   Carve c(ws);
   w.dz = c.take<bf16>((size_t)w.stride * dz_parts(act));
