@@ -263,6 +263,51 @@ def test_layernorm_many_rows_a_group(J, rows, h, dt):
         close(db, wb, (rows + 10) * U * np.abs(D).sum(0) + 1e-30)
 
 
+@pytest.mark.parametrize("h,res", [(16384, False), (16384, True), (12288, True), (14000, False), (9216, True)])
+def test_layernorm_bwd_rows_that_fill_the_ring(J, h, res):
+    """fp32 rows of which shared memory holds one or two at a time, several a CTA, through a list
+    with a bad entry."""
+    blk, rows, dt = 8, 640, torch.float32
+    S = rows + 9 * blk
+    x = randn(h, S, h, dt=dt, shift=1.0)
+    ga = randn(1, h, dt=dt, shift=1.0)
+    lst, rowsel = kept(S, blk, rows // blk, 3)
+    dres = randn(5, S, h, dt=dt) if res else None
+    _, mean, rstd = J.jenga_layernorm_fwd(x, ga, ga, idx=lst, blk=blk)
+    dy = randn(4, rows, h, dt=dt)
+    bad = rows // blk // 2
+    ok = torch.ones(rows, dtype=torch.bool, device="cuda")
+    for spoil in (False, True):
+        if spoil:
+            lst[bad] = S
+            ok[bad * blk:(bad + 2) * blk] = False  # the entry, and the next one, which is not above it
+        out = torch.full((S, h), 7.0, dtype=dt, device="cuda")
+        dx, dg, db = J.jenga_layernorm_bwd(dy, x, mean, rstd, ga, idx=lst, blk=blk, dres=dres, dx=out)
+        if spoil:
+            with pytest.raises(J._lib.JengaError):
+                J.jenga_check_device_status()
+        else:
+            J.jenga_check_device_status()
+        other = torch.ones(S, dtype=torch.bool, device="cuda")
+        other[rowsel[ok]] = False
+        assert (dx[other] == 7.0).all()
+        sel = rowsel[ok]
+        X, D, m, r = f64(x[sel]), f64(dy[ok]), f64(mean[ok]), f64(rstd[ok])
+        wx, wg, wb = od.layernorm_bwd(D, X, m, r, f64(ga))
+        n = np.abs((X - m[:, None]) * r[:, None])
+        g = np.abs(D * f64(ga))
+        q = h / 32 + 60
+        c1, c2 = g.mean(1, keepdims=True), (g * n).mean(1, keepdims=True)
+        tol = r[:, None] * (6 * U * g + (q + 6) * U * c1 + n * (q + 12) * U * c2)
+        if res:
+            E = f64(dres[sel])
+            wx, tol = wx + E, tol + 2 * U * np.abs(E)
+        tol = tol + (HALF[dt] + 4 * U) * np.abs(wx)
+        close(dx[sel], wx, tol * 1.01 + 1e-30)
+        close(dg, wg, (rows + 10) * U * (np.abs(D) * n).sum(0) + 1e-30)
+        close(db, wb, (rows + 10) * U * np.abs(D).sum(0) + 1e-30)
+
+
 def test_layernorm_unaligned_bases_and_in_place_gradients(J):
     bf = torch.bfloat16
     x, dy = randn(1, 90, 520, dt=bf), randn(2, 90, 520, dt=bf)

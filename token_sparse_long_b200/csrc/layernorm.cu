@@ -47,7 +47,11 @@ __device__ __forceinline__ uint4 pairs_vec(const uint64_t* f) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-constexpr int LN_MAX_STAGES = 8;
+// Rows in the ring.  More only queue up at the start, while the first warp, which issues them, should
+// be at its first row: 4096 x 4096 bf16, forward 16.3 us with eight and 15.0 with two, backward
+// 35.7 with six and 33.7 with four (two: 42, a stage of the backward is free a row later).
+constexpr int LN_FWD_STAGES = 2, LN_BWD_STAGES = 4;
+constexpr int LN_MAX_STAGES = 4;
 
 // Row group state of the ring: per stage a barrier and the sequence row (-1: a bad list
 // entry).
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 320 ? 2 : 1)
       ok = group_agree(ok, gw);
     }
     if (!ok) break;
-    if (gwarp == 0 && it > 0) {
+    if (gwarp == 0 && it > 0 && stages > 1) {
       start(r + (int64_t)(stages - 1) * G, s ? s - 1 : stages - 1);
       __syncwarp();
     }
@@ -370,6 +374,14 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 320 ? 2 : 1)
           }
           dst[i * step] = pairs_vec<T>(o);
         }
+      }
+    }
+    if (stages == 1) {  // rows so wide that the next one waits until all warps have left this one
+      ok = group_agree(ok, gw);
+      if (!ok) break;
+      if (gwarp == 0) {
+        start(r + G, 0);
+        __syncwarp();
       }
     }
     if (++s == stages) s = 0;
@@ -693,35 +705,43 @@ struct LnShape {
   int vec, nv, gw, groups, ctas, stages;
   size_t smem;
 };
+// Ring bytes of a CTA with per_sm of them on an SM: the SM's shared memory less what a CTA takes
+// besides.  (Without that allowance one CTA of eight did not fit and ran as a second wave: 768
+// wide, 104960 rows of bf16 backward 200 us against 138.)
+static int ln_room(int per_sm) {
+  const int room = 228 * 1024 / per_sm - 3 * 1024;
+  return room < 216 * 1024 ? room : 216 * 1024;
+}
 // Aligned forward.  bf16 is bound by instruction issue next to memory: 32 columns a thread spread
-// the per-row steps (barrier, shuffles, copies) over more of them, at 16 warps an SM (26240 x
+// the per-row steps (barrier, shuffles, copies) over more of them, at 16 warps an SM (with eight rows
+// in the ring, 26240 x
 // 4096: 78 us against 92 with 16 columns and 24 warps; 5120 wide: 94 against 122).  fp32 moves
 // twice the bytes a column: 16 columns, two CTAs an SM for wide rows (16384 x 4096: 83 us
 // against 93 with 32 columns, 101 with three CTAs).  Fewer columns when a warp holds the row.
 static LnShape ln_fwd_shape(int rows, int h, int es) {
   LnShape s{};
   s.vec = 16 / es;
-  const int nvec = h / s.vec, most = 4, room = 216 * 1024;  // 32 columns of bf16, 16 of fp32
+  const int nvec = h / s.vec, most = 4;  // 32 columns of bf16, 16 of fp32
   s.nv = 1;
   while (s.nv < most && nvec > 32 * s.nv) s.nv *= 2;
   s.gw = (nvec + 32 * s.nv - 1) / (32 * s.nv);
   s.groups = s.gw > 1 ? 1 : 4;
   const int warps = s.gw * s.groups, per_stage = h * es * s.groups;
   int per_sm = warps <= 4 ? (es == 2 ? 16 : 24) / warps : (es == 2 && warps <= 5 ? 3 : (warps <= (es == 2 ? 8 : 10) ? 2 : 1));
-  s.stages = room / (per_stage * per_sm);  // 3 rows of 64 KB at the least
-  s.stages = s.stages > LN_MAX_STAGES ? LN_MAX_STAGES : s.stages;
+  s.stages = ln_room(per_sm) / per_stage;  // 3 rows of 64 KB at the least
+  s.stages = s.stages > LN_FWD_STAGES ? LN_FWD_STAGES : s.stages;
   s.smem = (size_t)s.stages * per_stage;
   const int want = (rows - 1) / s.groups + 1, cap = per_sm * sm_count();
   s.ctas = want < cap ? want : cap;
   return s;
 }
 // Aligned backward: 16 columns a thread (gamma and the two sums stay in registers), eight warps a
-// CTA, fewer columns when a warp holds the row.  Unaligned rows, and aligned ones too wide for
-// two stages of the ring: one element a thread up to 512 threads.
+// CTA, fewer columns when a warp holds the row.  Rows too wide for two stages (fp32 above
+// 13824 columns, 9216 with dres) take one, without overlap in the CTA.  Unaligned rows: one element a
+// thread up to 512 threads.
 static LnShape ln_bwd_shape(int rows, int h, int es, bool aligned, int mats) {
   LnShape s{};
-  const int room = 216 * 1024;
-  aligned = aligned && 2 * h * es * mats <= room;
+  aligned = aligned && h * es * mats <= ln_room(1);
   s.vec = aligned ? 16 / es : 1;
   const int nvec = h / s.vec, most = aligned ? 16 / s.vec : 16;
   s.nv = 1;
@@ -731,9 +751,9 @@ static LnShape ln_bwd_shape(int rows, int h, int es, bool aligned, int mats) {
   const int warps = s.gw * s.groups, per_stage = h * es * mats * s.groups;
   int per_sm = !aligned ? 2 : (warps > 10 ? 1 : (warps < 8 ? 16 / warps : 2));
   if (aligned) {
-    while (per_sm > 1 && room / (per_stage * per_sm) < 3) --per_sm;  // one stage ahead while one drains
-    s.stages = room / (per_stage * per_sm);
-    s.stages = s.stages > LN_MAX_STAGES ? LN_MAX_STAGES : s.stages;
+    while (per_sm > 1 && ln_room(per_sm) / per_stage < 3) --per_sm;  // one stage ahead while one drains
+    s.stages = ln_room(per_sm) / per_stage;
+    s.stages = s.stages > LN_BWD_STAGES ? LN_BWD_STAGES : s.stages;
     s.smem = (size_t)s.stages * per_stage;
   }
   const size_t sums = s.groups > 1 ? (size_t)s.groups * 2 * h * sizeof(float) : 0;
