@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
       bulk_wait_group_read0();  // shared memory must outlive the reads
     }
   }
+  __syncwarp();  // roles of one lane rejoin their warp: the barrier and the release of tensor memory are collective
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -621,6 +622,7 @@ __global__ void __launch_bounds__(ABT_THREADS, 1)
       bulk_wait_group_read0();  // shared memory must outlive the reads
     }
   }
+  __syncwarp();  // roles of one lane rejoin their warp: the barrier and the release of tensor memory are collective
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

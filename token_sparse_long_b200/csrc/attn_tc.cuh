@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(ATC_THREADS, 1)
       if (lane == 0) mbar_arrive(&p_full[pb]);
     }
     const bool fin =
-        pair_all(ok && mbar_wait_at(&p_free[(nj - 1) & 1], ((nj - 1) >> 1) & 1, 109, (qt << 16) | nj), pair_bar);
+        pair_all(__all_sync(0xffffffffu, ok && mbar_wait_at(&p_free[(nj - 1) & 1], ((nj - 1) >> 1) & 1, 109, (qt << 16) | nj)),
+                 pair_bar);
     // merge the two halves' row sums (same maxima history, so they add directly)
     asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
     xm[hf * 128 + r] = l;
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(ATC_THREADS, 1)
       if (row_ok && hf == 0) lse[(int64_t)h * lse_ld + qrow] = -(m_used + __log2f(l_row));
     }
   }
+  __syncwarp();  // roles of one lane rejoin their warp: the barrier and the release of tensor memory are collective
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

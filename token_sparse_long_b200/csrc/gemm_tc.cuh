@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const float oscale = EPI == EPI_STORE_F32 ? ep.alpha * rfac : ep.alpha;
 #pragma unroll 1
         for (int c = 0; c < BN / 32; ++c) {
+          __syncwarp();  // the load is collective, the last step's stores went by lane
           tmem_ld32(tbase + c * 32, v);
           const int n = n0 + c * 32;
           if (EPI == EPI_STORE_F32 && ep.tma_out && n < N && m0 + quarter * 32 + 32 <= valid) {
@@ -431,6 +432,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll 1
           for (int hh = 0; hh < 2; ++hh) {
             float u[32];
+            __syncwarp();  // the loads are collective, the last step's stores went by lane
             tmem_ld32(tbase + g * 128 + hh * 32, v);
             tmem_ld32(tbase + g * 128 + 64 + hh * 32, u);
             const int n = n0 + g * 128;
@@ -460,6 +462,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         // acc column j (of ffn) -> group j/64, gate at 128*group + j%64, up at +64
 #pragma unroll 1
         for (int c = 0; c < BN / 32; ++c) {
+          __syncwarp();  // the load is collective, the last step's stores went by lane
           tmem_ld32(tbase + c * 32, v);
           const int j = n0 + c * 32;
           if (j >= N) continue;
@@ -549,6 +552,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 #pragma unroll 1
           for (int hh = 0; hh < 2; ++hh) {
             float u[32];
+            __syncwarp();  // the loads are collective, the last step's stores went by lane
             tmem_ld32(tbase + g * 128 + hh * 32, v);
             tmem_ld32(tbase + g * 128 + 64 + hh * 32, u);
             if (nh >= N) continue;
@@ -596,6 +600,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     }
     if (lane == 0 && nst > 0) bulk_wait_group_read<0>();  // staging outlives the stores' reads
   }
+  __syncwarp();  // roles of one lane rejoin their warp: the barrier and the release of tensor memory are collective
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -419,6 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
           // the tile's bias goes through shared memory: read per row from global memory its 64
           // loads a chunk cost 25 us at the end of a product.  A warp that timed out takes the
           // others with it here (the barrier carries the AND of `alive`).
+          __syncwarp();  // the last tile's stores branch by row
           if (!bar_and(alive, 1, 256)) break;
           const int q = (warp - 2) * 32 + lane;
           float bv = 0.f;
@@ -426,6 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
             if (p.bias && c0 + q < p.C) load_params<1>(p.bias, p.bias_bf16, c0 + q, 0.f, &bv);
             s_bias[q] = bv;
           }
+          __syncwarp();
           asm volatile("bar.sync 1, 256;" ::: "memory");
         }
         // the residual's first chunk is on its way before the product is ready
@@ -507,6 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
         for (int cc = 0; cc < BN / 128; ++cc) {
           const int n = cw + cc * 64;
           uint32_t raw[64];
+          __syncwarp();  // the loads below are collective
           tmem_ld32_nowait(lane_base + buf * ACC + cc * 64, raw);
           tmem_ld32_nowait(lane_base + buf * ACC + cc * 64 + 32, raw + 32);
           if (MW == 2 && hi - lo > 1) {  // the second warp's k-blocks

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(BM_THREADS, 1)
       if (mg < ngr && ng < ngr) part[((int64_t)b * ngr + ng) * ngr + mg] = best;
     }
   }
+  __syncwarp();  // roles of one lane rejoin their warp: the barrier and the release of tensor memory are collective
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
       // wait gave up
       my_ml[quad * 128 + r] = m;
       my_ml[(4 + quad) * 128 + r] = l;
+      __syncwarp();  // the chunk update above branches by row
       if (!bar_and(ok, 1, 32 * SF_EPI_WARPS)) break;
       if (quad == 0) {
         float mm = my_ml[r];
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * SF_EPI_WARPS) : "memory");
     }
   }
+  __syncwarp();  // roles of one lane rejoin their warp: the barrier and the release of tensor memory are collective
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
