@@ -106,8 +106,11 @@ __global__ void __launch_bounds__(BM_THREADS, 1)
     constexpr uint32_t idesc = umma_idesc_bf16(128, 128);
     for (int h = warp - 1; h < H; h += 2) {
       const int s = h % BM_STAGES, buf = h & 1;
-      if (!mbar_wait(&full[s], (uint32_t)((h / BM_STAGES) & 1), SITE_SCORE_TC)) break;
+      // The accumulator first: head h - 2 is read, so head h - 3, the stage's last content and the
+      // other warp's, has long landed.  A wait by parity on a stage whose last content were
+      // still on its way would pass at once.
       if (h >= 2 && !mbar_wait(&s_empty[buf], (uint32_t)(((h >> 1) - 1) & 1), SITE_SCORE_TC)) break;
+      if (!mbar_wait(&full[s], (uint32_t)((h / BM_STAGES) & 1), SITE_SCORE_TC)) break;
       tc_fence_after();
       const uint32_t qa = smem_u32(smem + s * BM_STAGE_BYTES);
       const uint32_t ka = qa + BM_TILE_BYTES;

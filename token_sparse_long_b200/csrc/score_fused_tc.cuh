@@ -276,11 +276,14 @@ __global__ void __launch_bounds__(SF_THREADS, 1)
         const long gp = P + p;
         if ((int)(gp & 1) != warp - 1) continue;
         const int s = (int)(gp % SF_STAGES), buf = (int)(gp & 1);
-        if (!mbar_wait(&full[s], (uint32_t)((gp / SF_STAGES) & 1), SITE_SCORE_TC)) {
+        // The accumulator first: pair gp - 2 is read, so pair gp - 3, the stage's last content and
+        // the other warp's, has long landed.  A wait by parity on a stage whose last content
+        // were still on its way would pass at once.
+        if (gp >= 2 && !mbar_wait(&s_empty[buf], (uint32_t)(((gp >> 1) - 1) & 1), SITE_SCORE_TC)) {
           ok = false;
           break;
         }
-        if (gp >= 2 && !mbar_wait(&s_empty[buf], (uint32_t)(((gp >> 1) - 1) & 1), SITE_SCORE_TC)) {
+        if (!mbar_wait(&full[s], (uint32_t)((gp / SF_STAGES) & 1), SITE_SCORE_TC)) {
           ok = false;
           break;
         }
