@@ -515,6 +515,12 @@ JENGA_API jenga_status jenga_test_exp2(const float* x, float* y_fma, float* y_mu
  * first (the default is 2 s) and restore it afterwards.  For tests only. */
 JENGA_API jenga_status jenga_test_wait_timeout(jenga_stream_t stream);
 
+/**
+ * jenga_test_linear_rows_shape -- how jenga_linear_fwd takes M (1 or 2) rows of x of K columns (a
+ * multiple of 8 up to 16384): warps per row of w, of the eight a CTA has, and stages of the ring that
+ * the rows of w pass through.  Host only.  For tests only. */
+JENGA_API jenga_status jenga_test_linear_rows_shape(int M, int K, int* warps_per_row, int* stages);
+
 #ifdef __cplusplus
 }
 #endif

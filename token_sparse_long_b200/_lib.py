@@ -118,6 +118,7 @@ _SIGS = {
                                 c_int, c_void_p]),
     "jenga_test_exp2": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_void_p]),
     "jenga_test_wait_timeout": (c_int, [c_void_p]),
+    "jenga_test_linear_rows_shape": (c_int, [c_int, c_int, POINTER(c_int), POINTER(c_int)]),
 }
 
 _lib = None

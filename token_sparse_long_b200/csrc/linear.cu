@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(288, 1)
     }
   asm volatile("bar.sync 2, 288;" ::: "memory");  // the barriers are ready
   bool ok = true;
-  int s = grp, ph = 0;  // the group's stage (stages >= groups)
+  int s = grp, ph = 0;  // the group's stage (stages is a multiple of groups)
   for (int b0 = lo, bi = 0; b0 < hi; b0 += GV_BATCH, bi ^= 1) {
     const int b1 = min(b0 + GV_BATCH, hi);
     // the value that this thread finishes below, and its bias
@@ -343,6 +343,24 @@ static size_t lin_part_bytes(const LinShape& s, int M, int N) {
 // Is the forward a pass over the rows of w (linear_rows)?  x as fp32 has to fit the registers of eight
 // warps; rows of w are copied whole, in multiples of 16 bytes.
 static bool lin_rows_ok(int M, int K) { return M <= 2 && K % 8 == 0 && K <= 16384; }
+
+// Ring of the rows pass: 128 registers of x a thread at the most, as few warps a row as that
+// allows, and a whole number of stages per group of warps, so that a stage always belongs to
+// one group: a group that met a stage after another group's row would wait by parity for a phase two
+// ahead, which passes at once while that row is still on its way.
+constexpr int GV_ROOM = 192 * 1024;
+struct LinRows {
+  int G, nv, stages;
+};
+static LinRows lin_rows_shape(int M, int K) {
+  LinRows r{1, 0, 0};
+  while ((K / 8 + 32 * r.G - 1) / (32 * r.G) > 16 / M) r.G *= 2;
+  r.nv = (K / 8 + 32 * r.G - 1) / (32 * r.G);
+  r.stages = GV_ROOM / (K * 2);
+  if (r.stages > GV_MAX_STAGES) r.stages = GV_MAX_STAGES;
+  r.stages -= r.stages % (8 / r.G);
+  return r;
+}
 
 // forward or dx: x side [M, red] (K-major), weight side [N, red] K-major or (WMN) [red, N]
 template <bool WMN>
@@ -494,31 +512,35 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
   cudaStream_t st = (cudaStream_t)stream;
   if (lin_rows_ok(M, K)) {
     p.m = M;
-    const int row = K * 2, room = 192 * 1024;
-    int stages = room / row;
-    stages = stages < GV_MAX_STAGES ? stages : GV_MAX_STAGES;
-    // 128 registers of x a thread at the most; as few warps a row as that allows
-    const int most = 16 / M;
-    int G = 1;
-    while ((K / 8 + 32 * G - 1) / (32 * G) > most) G *= 2;
-    const int nv = (K / 8 + 32 * G - 1) / (32 * G);
+    const LinRows r = lin_rows_shape(M, K);
     const unsigned grid = (unsigned)(N < sm_count() ? N : sm_count());
     const int ps = prof_begin("linear_rows", st);
     auto go = [&](auto kernel) {
-      const cudaError_t e = allow_smem((const void*)kernel, room);
+      const cudaError_t e = allow_smem((const void*)kernel, GV_ROOM);
       if (e == cudaSuccess)
-        kernel<<<grid, 288, (size_t)stages * row, st>>>((const bf16*)w, ldw, (const bf16*)x, ldx, N, K, G, stages, p);
+        kernel<<<grid, 288, (size_t)r.stages * K * 2, st>>>((const bf16*)w, ldw, (const bf16*)x, ldx, N, K, r.G, r.stages,
+                                                            p);
       return e;
     };
-    JENGA_CUDA_TRY(M == 1   ? (nv <= 4   ? go(linear_rows_kernel<1, 4>)
-                               : nv <= 8 ? go(linear_rows_kernel<1, 8>)
-                                         : go(linear_rows_kernel<1, 16>))
-                            : (nv <= 4 ? go(linear_rows_kernel<2, 4>) : go(linear_rows_kernel<2, 8>)));
+    JENGA_CUDA_TRY(M == 1   ? (r.nv <= 4   ? go(linear_rows_kernel<1, 4>)
+                               : r.nv <= 8 ? go(linear_rows_kernel<1, 8>)
+                                           : go(linear_rows_kernel<1, 16>))
+                            : (r.nv <= 4 ? go(linear_rows_kernel<2, 4>) : go(linear_rows_kernel<2, 8>)));
     prof_end(ps, st);
     JENGA_LAUNCH_CHECK();
     return JENGA_OK;
   }
   return lin_out<false>(shape, x, ldx, w, ldw, M, N, K, p, ws, "linear_fwd", st);
+}
+
+// Test hook: the rows pass's warps per row and ring stages for M rows of x of K columns.
+extern "C" jenga_status jenga_test_linear_rows_shape(int M, int K, int* warps_per_row, int* stages) {
+  JENGA_CHECK_ARG(warps_per_row && stages && M >= 1 && K >= 1 && lin_rows_ok(M, K),
+                  "jenga_test_linear_rows_shape: M=%d K=%d", M, K);
+  const LinRows r = lin_rows_shape(M, K);
+  *warps_per_row = r.G;
+  *stages = r.stages;
+  return JENGA_OK;
 }
 
 extern "C" size_t jenga_linear_bwd_workspace_bytes(int M, int N, int K, jenga_activation act) {
