@@ -52,3 +52,42 @@ def test_linear_rows_ring_wraps(J, M, N, K):
     assert torch.equal(y, pre)
     for _ in range(3):
         assert torch.equal(J.jenga_linear_fwd(x, w, b)[0], y)
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 32000, 2880), (50, 40000, 320), (100, 40000, 960), (20000, 128, 320), (16, 40000, 40),
+                                   (128, 40001, 64), (20000, 100, 64), (9, 33000, 200)])
+def test_linear_odd_k_blocks_and_several_tiles_a_cluster(J, M, N, K):
+    """Products whose tiles have an odd number of 64-deep k-blocks and of which a CTA pair takes
+    several: the two issuing warps change places from tile to tile."""
+    x, w, b = randn(1, M, K), randn(2, N, K, scale=1.5 / K ** 0.5), randn(3, N, dt=torch.float32)
+    y, _ = J.jenga_linear_fwd(x, w, b)
+    J.jenga_check_device_status()
+    want = x.double() @ w.double().T + b.double()
+    S = x.double().abs() @ w.double().abs().T + b.double().abs()
+    close(y, want, 2 * (K + 4) * U * S + RB * want.abs() * 1.001)
+    for _ in range(3):
+        assert torch.equal(J.jenga_linear_fwd(x, w, b)[0], y)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("M,N,K", [(832, 1024, 4096), (40, 1024, 4096), (200, 1100, 3904), (16, 2880, 32000), (100, 960, 20000)])
+def test_linear_bwd_odd_k_blocks_and_several_tiles_a_cluster(J, M, N, K, act):
+    x, w, dy, z = randn(1, M, K), randn(2, N, K, scale=1.5 / N ** 0.5), randn(3, M, N), randn(4, M, N)
+    dx, dw, db = J.jenga_linear_bwd(dy, x, w, act=act, pre=None if act == "none" else z)
+    J.jenga_check_device_status()
+    dz, e = dy.double(), 0.0
+    if act == "silu":
+        s = torch.sigmoid(z.double())
+        dz = dz * s * (1 + z.double() * (1 - s))
+        # __expf is within 2 + 1.173 |z| ulp; slope <= 1.13, the products round a few times
+        e = dy.double().abs() * (24 + 3 * z.double().abs()) * U
+    D, X, W = dz.abs(), x.double().abs(), w.double().abs()
+    smooth = RB if act == "silu" else 0.0  # dx takes dz as one bf16 operand
+    want = dz @ w.double()
+    close(dx, want, 1.01 * ((e + smooth * D) @ W + 2 * (N + 4) * U * (D @ W)) + RB * want.abs() * 1.001 + 1e-30)
+    n = min(512, M) + M / 512 + 8
+    close(dw, dz.T @ x.double(), 1.01 * ((e + 2 * U * D).T @ X + 2 * n * U * (D.T @ X)) + 1e-30)
+    close(db, dz.sum(0), ((e + D * 0).sum(0) + (M + 4) * U * D.sum(0)) * 1.01)
+    for _ in range(3):
+        for a, b in zip(J.jenga_linear_bwd(dy, x, w, act=act, pre=None if act == "none" else z), (dx, dw, db)):
+            assert torch.equal(a, b)

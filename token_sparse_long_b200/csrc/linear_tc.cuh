@@ -23,7 +23,11 @@
 //   warps 2..9  epilogue: two warps per TMEM lane quarter, half of the columns each
 //   warp 10     in the leader, the MMAs of every other k-block of a narrow tile, into an
 //               accumulator of its own that the epilogue adds: a warp issues an MMA only
-//               every 116 clocks or so, which is more than a tile of 128 columns needs
+//               every 116 clocks or so, which is more than a tile of 128 columns needs.  The
+//               k-blocks alternate over the whole launch, not within a tile: a ring of an even
+//               number of stages then keeps each stage with one of the two warps.  (Taken by a
+//               warp that had not seen the stage's last phase, a wait by parity passes while that
+//               phase is still open.)
 // Persistent: one cluster per SM pair walks the tiles in bands of 8 row tiles (row tile
 // fastest), so that a wave's operands stay within L2.
 #pragma once
@@ -228,6 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
   using L = LinSmem<BN, SWAP>;
   static_assert(!(BMN && BN < 128), "an MN-major B half is at least one 64-wide box");
   constexpr int ST = L::STAGES, MW = lin_mma_warps<BN>, ACC = MW * BN;  // columns of an accumulator set
+  static_assert(ST % MW == 0 && LT_CHUNK % MW == 0, "a ring stage belongs to one MMA warp");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -339,8 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
       for (int i = g > ST ? g - ST : 0; i < g; ++i)
         if (!pair_wait(&full[i % ST], (i / ST) & 1)) break;
   } else if ((warp == 1 || warp == 10) && rank == 0) {
-    // ---------------- MMA issuers (leader): warp mw takes k-blocks mw, mw + MW, ... of each unit (a
-    // tile, or a chunk of LIN_GRAD)
+    // ---------------- MMA issuers (leader): warp mw takes every MW-th k-block of the launch, those
+    // of a unit (a tile, or a chunk of LIN_GRAD) into the unit's accumulator mw
     const int mw = warp == 1 ? 0 : 1;
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
                            ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
@@ -358,7 +363,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
         }
         tc_fence_after();
         const uint32_t acc = tmem + buf * ACC + mw * BN;
-        for (int kb = u0 + mw; kb < u1; kb += MW) {
+        const int kb0 = u0 + ((g + u0 - lo + mw) & (MW - 1));  // the warp's first of the unit
+        for (int kb = kb0; kb < u1; kb += MW) {
           const int gk = g + kb - lo, s = gk % ST;
           if (!__all_sync(0xffffffffu, pair_wait(&full[s], (gk / ST) & 1))) {
             ok = false;
@@ -372,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
             for (int k = 0; k < 4; ++k) {
               const uint64_t da = AMN ? umma_desc_mn_sw128(sa + k * 2048, 8192) : umma_desc_k_sw128(sa + k * 32);
               const uint64_t db = BMN ? umma_desc_mn_sw128(sb + k * 2048, 8192) : umma_desc_k_sw128(sb + k * 32);
-              umma_pair(acc, da, db, idesc, (kb > u0 + mw || k > 0) ? 1u : 0u);
+              umma_pair(acc, da, db, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
             }
             umma_commit_pair(&empty[s]);
           }
@@ -406,10 +412,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
       if (lane == 0) bulk_commit_group();
       ++nst;
     };
-    int it = 0;
+    int it = 0, g = 0;  // units and k-blocks before the tile
     for (int t = cluster; t < ntiles; t += nclusters) {
       int r0, c0, lo, hi;
       tile_at(t, r0, c0, lo, hi);
+      // accumulator of the tile's (and of each of its chunks') first k-block, and the other one's offset
+      const int acc1 = (g & (MW - 1)) * BN, acc2 = ACC - BN - acc1;
+      g += hi - lo;
       const int rw = r0 + (int)rank * 128 + quarter * 32;  // the warp's first row
       const int r = rw + lane;
       const int cw = c0 + half * (BN / 2);                 // the warp's first column
@@ -455,10 +464,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
             const int m0 = cw + cc * 16;
             uint32_t raw[16];
             __syncwarp();  // the load below is collective
-            tmem_ld16_nowait(lane_base + buf * ACC + cc * 16, raw);
-            if (MW == 2 && hi - lo > 1) {  // the second warp's k-blocks
+            tmem_ld16_nowait(lane_base + buf * ACC + acc1 + cc * 16, raw);
+            if (MW == 2 && hi - lo > 1) {  // the other warp's k-blocks
               uint32_t more[16];
-              tmem_ld16_nowait(lane_base + buf * ACC + BN + cc * 16, more);
+              tmem_ld16_nowait(lane_base + buf * ACC + acc2 + cc * 16, more);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) + __uint_as_float(more[i]));
@@ -510,12 +519,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
           const int n = cw + cc * 64;
           uint32_t raw[64];
           __syncwarp();  // the loads below are collective
-          tmem_ld32_nowait(lane_base + buf * ACC + cc * 64, raw);
-          tmem_ld32_nowait(lane_base + buf * ACC + cc * 64 + 32, raw + 32);
-          if (MW == 2 && hi - lo > 1) {  // the second warp's k-blocks
+          tmem_ld32_nowait(lane_base + buf * ACC + acc1 + cc * 64, raw);
+          tmem_ld32_nowait(lane_base + buf * ACC + acc1 + cc * 64 + 32, raw + 32);
+          if (MW == 2 && hi - lo > 1) {  // the other warp's k-blocks
             uint32_t more[64];
-            tmem_ld32_nowait(lane_base + buf * ACC + BN + cc * 64, more);
-            tmem_ld32_nowait(lane_base + buf * ACC + BN + cc * 64 + 32, more + 32);
+            tmem_ld32_nowait(lane_base + buf * ACC + acc2 + cc * 64, more);
+            tmem_ld32_nowait(lane_base + buf * ACC + acc2 + cc * 64 + 32, more + 32);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 64; ++i) raw[i] = __float_as_uint(__uint_as_float(raw[i]) + __uint_as_float(more[i]));
@@ -655,12 +664,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin_threads<BN>, 1)
 #pragma unroll
           for (int c = 0; c < BN / 64; ++c) {
             uint32_t raw[32];
-            tmem_ld32_nowait(lane_base + buf * ACC + c * 32, raw);
+            tmem_ld32_nowait(lane_base + buf * ACC + acc1 + c * 32, raw);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[c * 32 + i] += __uint_as_float(raw[i]);
-            if (MW == 2 && hi - kb > 1) {  // the second warp's k-blocks
-              tmem_ld32_nowait(lane_base + buf * ACC + BN + c * 32, raw);
+            if (MW == 2 && hi - kb > 1) {  // the other warp's k-blocks
+              tmem_ld32_nowait(lane_base + buf * ACC + acc2 + c * 32, raw);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) acc[c * 32 + i] += __uint_as_float(raw[i]);
