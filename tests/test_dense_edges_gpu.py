@@ -91,3 +91,24 @@ def test_linear_bwd_odd_k_blocks_and_several_tiles_a_cluster(J, M, N, K, act):
     for _ in range(3):
         for a, b in zip(J.jenga_linear_bwd(dy, x, w, act=act, pre=None if act == "none" else z), (dx, dw, db)):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ counts near 2^31
+def test_layernorm_as_many_rows_as_an_int_holds(J):
+    if torch.cuda.get_device_properties(0).total_memory < 60 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    rows = 2 ** 31 - 1
+    x = torch.ones(rows, 1, dtype=BF, device="cuda")
+    dy = torch.zeros(rows, 1, dtype=BF, device="cuda")
+    at = torch.tensor([0, 1, 2 ** 30, rows - 2400, rows - 2, rows - 1], device="cuda")
+    dy[at] = 1.0
+    mean, rstd = (torch.full((rows,), v, device="cuda") for v in (0.5, 2.0))
+    # h = 1, n = (1 - 1/2) 2 = 1: dx = rstd (g - g - n g n) = -2 dy, exact in every step
+    dx, dg, db = J.jenga_layernorm_bwd(dy, x, mean, rstd)
+    J.jenga_check_device_status()
+    assert (dx[at] == -2.0).all() and float(dg) == 6.0 and float(db) == 6.0
+    assert int((dx != 0).sum()) == 6
+    del dx, dy, mean, rstd
+    y, mean, rstd = J.jenga_layernorm_fwd(x, eps=0.25)
+    J.jenga_check_device_status()
+    assert not y.any() and bool((mean == 1.0).all()) and bool((rstd == 2.0).all())

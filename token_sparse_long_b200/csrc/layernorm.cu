@@ -547,10 +547,10 @@ __global__ void __launch_bounds__(MAXT)
     }
     if (t0 + i * step < nvec) load_params<VEC>(gamma, wbf16, (int64_t)(t0 + i * step) * VEC, 1.f, ga[i]);
   }
-  auto fetch = [&](BwdRow<T, NV>& b, int r) {
+  auto fetch = [&](BwdRow<T, NV>& b, int64_t r) {  // 64 bits: a row count near 2^31 plus a step
     b.row = -1;
     if (r >= valid) return;
-    b.row = sequence_row(map, r);
+    b.row = sequence_row(map, (int)r);
     if (b.row < 0) {
       if (t0 == 0) record_device_error(JENGA_EINTERNAL, SITE_INDEX_RANGE, (unsigned)r);
       return;
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(MAXT)
       b.dy[i].zero();
       if (t0 + i * step < nvec) {
         b.x[i].load(x + b.row * ldx + c);
-        b.dy[i].load(dy + (int64_t)r * ldy + c);
+        b.dy[i].load(dy + r * ldy + c);
         if (RES) b.res[i].load(dres + b.row * ldr + c);
       }
     }
@@ -574,10 +574,10 @@ __global__ void __launch_bounds__(MAXT)
   const int lw = lane & (p2 - 1);
   const float inv_h = 1.f / (float)h;
   BwdRow<T, NV> cur, nxt;
-  const int r0 = blockIdx.x * groups + grp;
+  const int64_t r0 = blockIdx.x * groups + grp;
   fetch(cur, r0);
   int par = 0;
-  for (int r = r0; r < valid; r += G) {
+  for (int64_t r = r0; r < valid; r += G) {
     fetch(nxt, r + G);
     if (cur.row >= 0) {
       float s1 = 0.f, s2 = 0.f;
