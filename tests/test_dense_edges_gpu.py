@@ -112,3 +112,25 @@ def test_layernorm_as_many_rows_as_an_int_holds(J):
     y, mean, rstd = J.jenga_layernorm_fwd(x, eps=0.25)
     J.jenga_check_device_status()
     assert not y.any() and bool((mean == 1.0).all()) and bool((rstd == 2.0).all())
+
+
+# ------------------------------------------------------------------ infinities, NaN, far tails
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("M,N,K", [(200, 72, 64), (200, 67, 64)])
+def test_linear_bwd_infinite_and_nan_gradients(J, act, M, N, K):
+    """An infinite dz makes its row of dw infinite, its column of db and its row of dx; a NaN makes them NaN."""
+    x, w, dy = randn(1, M, K), randn(2, N, K), randn(3, M, N)
+    z = randn(4, M, N).abs() + 0.5  # slopes above 0
+    dy[7, 3], dy[9, 5], dy[30, 40] = math.inf, -math.inf, math.nan
+    dx, dw, db = J.jenga_linear_bwd(dy, x, w, act=act, pre=None if act == "none" else z)
+    J.jenga_check_device_status()
+    assert torch.equal(dw[3], x[7].float() * math.inf) and torch.equal(dw[5], x[9].float() * -math.inf)
+    assert db[3] == math.inf and db[5] == -math.inf
+    assert torch.isnan(dw[40]).all() and torch.isnan(db[40]) and torch.isnan(dx[30]).all()
+    assert torch.equal(dx[7].float(), w[3].float() * math.inf) and torch.equal(dx[9].float(), w[5].float() * -math.inf)
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[[3, 5, 40]] = False
+    assert torch.isfinite(dw[rest]).all() and torch.isfinite(db[rest]).all()
+    rows = torch.ones(M, dtype=torch.bool, device="cuda")
+    rows[[7, 9, 30]] = False
+    assert torch.isfinite(dx[rows]).all()

@@ -78,9 +78,12 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
               if (c + i * CSTEP < N) RowVec<bf16, PER>::store(o + q * part_stride + i * CSTEP, d + i * PER);
-            if (q + 1 < PARTS) {
+            if (q + 1 < PARTS) {  // what the rounding left; nothing of an infinity or a NaN
 #pragma unroll
-              for (int e = 0; e < 8; ++e) d[e] -= __bfloat162float(__float2bfloat16_rn(d[e]));
+              for (int e = 0; e < 8; ++e) {
+                const float hi = __bfloat162float(__float2bfloat16_rn(d[e]));
+                d[e] = fabsf(hi) < INFINITY ? d[e] - hi : 0.f;
+              }
             }
           }
         }
