@@ -134,3 +134,53 @@ def test_linear_bwd_infinite_and_nan_gradients(J, act, M, N, K):
     rows = torch.ones(M, dtype=torch.bool, device="cuda")
     rows[[7, 9, 30]] = False
     assert torch.isfinite(dx[rows]).all()
+
+
+def _phi(z):
+    return torch.special.ndtr(z), torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+
+
+@pytest.mark.parametrize("M", [1, 3, 300])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_activation_tails_are_relatively_exact(J, act, M):
+    """y = act(z) for one z a column, far into the tail where act(z) is tiny: a bf16 rounding and a
+    few fp32 ones relative to y itself.  erfcf is within 4 ulp, its rounded argument adds
+    1.3 (1 + z^2) half ulp; __expf is within 2 + 1.173 |z| ulp."""
+    lo = -12.0 if act == "gelu" else -80.0
+    z = torch.linspace(lo, 8.0, 520, device="cuda").to(BF)
+    w = torch.zeros(520, 8, dtype=BF, device="cuda")
+    w[:, 0] = z
+    x = torch.zeros(M, 8, dtype=BF, device="cuda")
+    x[:, 0] = 1.0
+    y, _ = J.jenga_linear_fwd(x, w, act=act)
+    J.jenga_check_device_status()
+    Z = z.double()
+    want = Z * torch.special.ndtr(Z) if act == "gelu" else Z * torch.sigmoid(Z)
+    rel = (1.3 * (1 + Z * Z) + 16) * U if act == "gelu" else (10 + 2.4 * Z.abs()) * U
+    close(y, want.expand(M, -1), (want.abs() * (rel + RB * 1.001)).expand(M, -1))
+    assert (y[0][z < -4] != 0).all()
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_activation_slopes_in_the_tails_and_at_infinity(J, act):
+    z = torch.linspace(-12.0, 8.0, 518, device="cuda").to(BF)
+    z = torch.cat([z, torch.tensor([math.inf, -math.inf], device="cuda", dtype=BF)])[None].contiguous()
+    dy = torch.ones_like(z)
+    x, w = randn(1, 1, 8), randn(2, 520, 8)
+    dx, dw, db = J.jenga_linear_bwd(dy, x, w, act=act, pre=z)
+    J.jenga_check_device_status()
+    assert db[518] == 1.0 and db[519] == 0.0
+    assert torch.isfinite(dx).all() and torch.equal(dw[518], x[0].float()) and not dw[519].any()
+    Z = z[0, :518].double()
+    if act == "gelu":
+        P, f = _phi(Z)
+        want = P + Z * f
+        tol = P * (1.3 * (1 + Z * Z) + 12) * U + (Z * f).abs() * (2.2 * Z * Z + 14) * U
+    else:
+        s = torch.sigmoid(Z)
+        want = s * (1 + Z * (1 - s))
+        # s carries the exponential's error; 1 - s and 1 + z (1 - s) add roundings of their operands
+        tol = (s + (Z * s * (1 - s)).abs() + (Z * s * s).abs()) * (12 + 2.4 * Z.abs()) * U
+    close(db[:518], want, tol)
+    # three bf16 parts: two truncated adds and a rounded one on top of dz's error
+    close(dw[:518], want[:, None] * x.double(), (tol + 8 * U * want.abs())[:, None] * x.double().abs() + 1e-30)
