@@ -405,7 +405,8 @@ JENGA_API jenga_status jenga_lm_loss_segmented(const void* hidden, const void* w
  * is recorded and its rows are skipped (a block listed twice leaves its rows undefined).  rows
  * must be whole blocks when idx or n_kept is given; blk is 1 or more and otherwise unused.
  * Pitches (ld*) are in elements.  An output may be the same matrix as an input (same pointer
- * and pitch) where stated, and must not overlap one otherwise (JENGA_EINVAL).
+ * and pitch) where stated.  Otherwise outputs and the workspace share no byte with an input or
+ * with one another (JENGA_EINVAL); columns side by side of rows of one pitch do not.
  * rows = 0 is a call without work (overwritten gradients become zeros). */
 
 /* jenga_layernorm_fwd -- y[r] = (x[r] - mean) * rstd * gamma + beta per row of h elements, with

@@ -184,3 +184,30 @@ def test_activation_slopes_in_the_tails_and_at_infinity(J, act):
     close(db[:518], want, tol)
     # three bf16 parts: two truncated adds and a rounded one on top of dz's error
     close(dw[:518], want[:, None] * x.double(), (tol + 8 * U * want.abs())[:, None] * x.double().abs() + 1e-30)
+
+
+# ------------------------------------------------------------------ columns of one matrix
+def test_inputs_and_outputs_side_by_side_in_one_matrix(J):
+    M, K, N = 300, 264, 200
+    b = torch.full((M, K + N + N + 8), math.nan, dtype=BF, device="cuda")
+    x, y, pre = b[:, :K], b[:, K:K + N], b[:, K + N:K + 2 * N]
+    w, dy = randn(2, N, K, scale=0.1), randn(3, M, N)
+    x0 = randn(1, M, K)
+    x.copy_(x0)
+    want, wpre = J.jenga_linear_fwd(x0, w, act="gelu", save_pre=True)
+    J.jenga_linear_fwd(x, w, act="gelu", out=y, pre=pre)
+    assert torch.equal(y, want) and torch.equal(pre, wpre) and torch.equal(x, x0)
+    ref = J.jenga_linear_bwd(dy, x0, w, act="gelu", pre=wpre)
+    y.copy_(dy)
+    dx = torch.full((M, 2 * K), math.nan, dtype=BF, device="cuda")
+    dx[:, K:] = x0
+    got = J.jenga_linear_bwd(y, dx[:, K:], w, act="gelu", pre=pre, dx=dx[:, :K])
+    assert all(torch.equal(a, c) for a, c in zip(got, ref)) and torch.equal(dx[:, K:], x0)
+    ln = torch.full((M, 2 * K), math.nan, dtype=BF, device="cuda")
+    ln[:, :K] = x0
+    J.jenga_layernorm_fwd(ln[:, :K], out=ln[:, K:])
+    assert torch.equal(ln[:, K:], J.jenga_layernorm_fwd(x0)[0]) and torch.equal(ln[:, :K], x0)
+    J.jenga_dropout(ln[:, :K], 0.3, 5, 6, out=ln[:, K:])
+    assert torch.equal(ln[:, K:], J.jenga_dropout(x0, 0.3, 5, 6)) and torch.equal(ln[:, :K], x0)
+    assert torch.isnan(b[:, K + 2 * N:]).all()
+    J.jenga_check_device_status()

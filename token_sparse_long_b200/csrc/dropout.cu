@@ -170,9 +170,9 @@ extern "C" jenga_status jenga_dropout(const void* x, int64_t ldx, const void* re
   if (rows == 0) return JENGA_OK;
   JENGA_CHECK_ARG(x && y, "jenga_dropout: null pointer");
   const int es = dt == JENGA_F32 ? 4 : 2;
-  const uint64_t ny = span_bytes(rows, cols, ldy, es);
-  JENGA_CHECK_ARG(alias_ok(y, ldy, ny, x, ldx, span_bytes(rows, cols, ldx, es), true) &&
-                      alias_ok(y, ldy, ny, residual, ldr, span_bytes(rows, cols, ldr, es), true),
+  JENGA_CHECK_ARG(outputs_apart({mat_span(y, rows, cols, ldy, es)},
+                                {mat_span(x, rows, cols, ldx, es, true), mat_span(residual, rows, cols, ldr, es, true),
+                                 vec_span(idx, rows / blk, 4), vec_span(n_kept, 1, 4)}),
                   "jenga_dropout: y overlaps an input other than as the same matrix");
   const int v = 16 / es;
   const bool vec = cols % v == 0 && ldx % v == 0 && ldy % v == 0 && (!residual || ldr % v == 0) && is16(x) && is16(y) &&

@@ -918,8 +918,12 @@ extern "C" jenga_status jenga_layernorm_fwd(const void* x, int64_t ldx, int S, i
   if (rows == 0) return JENGA_OK;
   JENGA_CHECK_ARG(x && y, "jenga_layernorm_fwd: null pointer");
   const int es = dt == JENGA_F32 ? 4 : 2;
-  JENGA_CHECK_ARG(alias_ok(y, ldy, span_bytes(rows, h, ldy, es), x, ldx, span_bytes(S, h, ldx, es), !idx),
-                  "jenga_layernorm_fwd: y overlaps x (allowed only as the same matrix, without a block list)");
+  const int wes = wdt == JENGA_F32 ? 4 : 2;
+  JENGA_CHECK_ARG(outputs_apart({mat_span(y, rows, h, ldy, es), vec_span(mean, rows, 4), vec_span(rstd, rows, 4)},
+                                {mat_span(x, idx ? S : rows, h, ldx, es, !idx), vec_span(gamma, h, wes),
+                                 vec_span(beta, h, wes), vec_span(idx, rows / blk, 4), vec_span(n_kept, 1, 4)}),
+                  "jenga_layernorm_fwd: an output overlaps an input or another output (allowed only for y = x, the same "
+                  "matrix, without a block list)");
   const int v = 16 / es;
   const bool aligned =
       h % v == 0 && ldx % v == 0 && ldy % v == 0 && is16(x) && is16(y) && is16(gamma) && is16(beta);
@@ -964,15 +968,22 @@ extern "C" jenga_status jenga_layernorm_bwd(const void* dy, int64_t ldy, const v
   }
   JENGA_CHECK_ARG(dy && x && mean && rstd && dx, "jenga_layernorm_bwd: null pointer");
   const int es = dt == JENGA_F32 ? 4 : 2;
-  const uint64_t nd = span_bytes(idx ? S : rows, h, ldd, es);
-  JENGA_CHECK_ARG(alias_ok(dx, ldd, nd, x, ldx, span_bytes(idx ? S : rows, h, ldx, es), true) &&
-                      alias_ok(dx, ldd, nd, dy, ldy, span_bytes(rows, h, ldy, es), !idx) &&
-                      alias_ok(dx, ldd, nd, dres, ldr, span_bytes(idx ? S : rows, h, ldr, es), true),
-                  "jenga_layernorm_bwd: dx overlaps an input other than as the same matrix");
+  const int64_t xrows = idx ? S : rows;
+  const auto apart = [&](size_t ws_used) {  // dx as a row operand is compact or, through a list, the sequence
+    return outputs_apart(
+        {mat_span(dx, xrows, h, ldd, es), vec_span(dgamma, h, 4), vec_span(dbeta, h, 4), vec_span(ws, ws_used, 1)},
+        {mat_span(x, xrows, h, ldx, es, true), mat_span(dy, rows, h, ldy, es, !idx),
+         mat_span(dres, xrows, h, ldr, es, true), vec_span(mean, rows, 4), vec_span(rstd, rows, 4),
+         vec_span(gamma, h, wdt == JENGA_F32 ? 4 : 2), vec_span(idx, rows / blk, 4), vec_span(n_kept, 1, 4)});
+  };
+  const char* met = "jenga_layernorm_bwd: an output or the workspace overlaps an input or another output (allowed only "
+                    "for dx as the same matrix as dres, x or, without a block list, dy)";
+  JENGA_CHECK_ARG(apart(0), "%s", met);
   const bool wgrad = dgamma || dbeta;
   const size_t need = jenga_layernorm_bwd_workspace_bytes(rows, h);
   if (wgrad && (!ws || ws_bytes < need))
     return fail(JENGA_EWORKSPACE, "jenga_layernorm_bwd: workspace %zu < %zu", ws ? ws_bytes : (size_t)0, need);
+  JENGA_CHECK_ARG(!wgrad || apart(need), "%s", met);
   float* part = wgrad ? (float*)(((uintptr_t)ws + 255) & ~uintptr_t(255)) : nullptr;
   const int v = 16 / es;
   const bool aligned = h % v == 0 && ldx % v == 0 && ldy % v == 0 && ldd % v == 0 && (!dres || ldr % v == 0) &&

@@ -489,17 +489,20 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
   JENGA_CHECK_ARG(x && w && y, "jenga_linear_fwd: null pointer");
   JENGA_CHECK_ARG(lin_operand_ok(x, ldx) && lin_operand_ok(w, ldw),
                   "jenga_linear_fwd: x and w need 16-byte aligned rows (pitch a multiple of 8)");
-  const uint64_t ny = span_bytes(M, N, ldy, 2), np = span_bytes(M, N, ldp, 2), nx = span_bytes(M, K, ldx, 2),
-                 nw = span_bytes(N, K, ldw, 2), nr = span_bytes(M, N, ldr, 2);
-  JENGA_CHECK_ARG(alias_ok(y, ldy, ny, x, ldx, nx, false) && alias_ok(y, ldy, ny, w, ldw, nw, false) &&
-                      alias_ok(y, ldy, ny, residual, ldr, nr, true) && alias_ok(y, ldy, ny, pre, ldp, np, false) &&
-                      alias_ok(pre, ldp, np, x, ldx, nx, false) && alias_ok(pre, ldp, np, w, ldw, nw, false) &&
-                      alias_ok(pre, ldp, np, residual, ldr, nr, false),
-                  "jenga_linear_fwd: an output overlaps an input (only y = residual, the same matrix, is allowed)");
+  const auto apart = [&](size_t ws_used) {
+    return outputs_apart(
+        {mat_span(y, M, N, ldy, 2), mat_span(pre, M, N, ldp, 2), vec_span(ws, ws_used, 1)},
+        {mat_span(residual, M, N, ldr, 2, true), mat_span(x, M, K, ldx, 2), mat_span(w, N, K, ldw, 2),
+         vec_span(bias, N, bias_dt == JENGA_F32 ? 4 : 2), vec_span(n_kept, 1, 4)});
+  };
+  const char* met = "jenga_linear_fwd: an output or the workspace overlaps an input or another output (allowed only for "
+                    "y = residual, the same matrix)";
+  JENGA_CHECK_ARG(apart(0), "%s", met);
   const LinShape shape = lin_shape(M, N, K);
   const size_t need = jenga_linear_fwd_workspace_bytes(M, N, K);
   if (need && (!ws || ws_bytes < need))
     return fail(JENGA_EWORKSPACE, "jenga_linear_fwd: workspace %zu < %zu", ws ? ws_bytes : (size_t)0, need);
+  JENGA_CHECK_ARG(!need || apart(need), "%s", met);
   LinArgs p{};
   p.n_kept = n_kept;
   p.blk = blk;
@@ -574,16 +577,18 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
   if (act == JENGA_ACT_NONE) pre = nullptr;
   if (!dw) x = nullptr;
   if (!dx) w = nullptr;
-  const uint64_t nd = span_bytes(M, K, ldd, 2), ndw = span_bytes(N, K, lddw, 4), ndy = span_bytes(M, N, ldy, 2),
-                 np = span_bytes(M, N, ldp, 2), nx = span_bytes(M, K, ldx, 2), nw = span_bytes(N, K, ldw, 2);
-  JENGA_CHECK_ARG(alias_ok(dx, ldd, nd, dy, ldy, ndy, false) && alias_ok(dx, ldd, nd, x, ldx, nx, false) &&
-                      alias_ok(dx, ldd, nd, w, ldw, nw, false) && alias_ok(dx, ldd, nd, pre, ldp, np, false) &&
-                      alias_ok(dw, lddw, ndw, dy, ldy, ndy, false) && alias_ok(dw, lddw, ndw, x, ldx, nx, false) &&
-                      alias_ok(dw, lddw, ndw, w, ldw, nw, false) && alias_ok(dw, lddw, ndw, pre, ldp, np, false),
-                  "jenga_linear_bwd: an output overlaps an input");
+  const auto apart = [&](size_t ws_used) {
+    return outputs_apart({mat_span(dx, M, K, ldd, 2), mat_span(dw, N, K, lddw, 4), vec_span(db, N, 4),
+                          vec_span(ws, ws_used, 1)},
+                         {mat_span(dy, M, N, ldy, 2), mat_span(x, M, K, ldx, 2), mat_span(w, N, K, ldw, 2),
+                          mat_span(pre, M, N, ldp, 2), vec_span(n_kept, 1, 4)});
+  };
+  const char* met = "jenga_linear_bwd: an output or the workspace overlaps an input or another output";
+  JENGA_CHECK_ARG(apart(0), "%s", met);
   const size_t need = jenga_linear_bwd_workspace_bytes(M, N, K, act);
   if (!ws || ws_bytes < need)
     return fail(JENGA_EWORKSPACE, "jenga_linear_bwd: workspace %zu < %zu", ws ? ws_bytes : (size_t)0, need);
+  JENGA_CHECK_ARG(apart(need), "%s", met);
   const LinBwdWs W = lin_bwd_carve(ws, M, N, K, act);
   // dy itself is the operand when nothing has to be computed, aligned or cut off at a device count
   const bool direct = act == JENGA_ACT_NONE && !n_kept && lin_operand_ok(dy, ldy);

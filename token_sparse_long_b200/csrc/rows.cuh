@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <initializer_list>
 
 #include "common.cuh"
 
@@ -186,18 +187,39 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ------------------------------------------------------------------ host checks
-// Bytes of a [rows, cols] matrix with row pitch ld.
-inline uint64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int es) {
-  return rows < 1 || cols < 1 ? 0 : ((uint64_t)(rows - 1) * ld + cols) * es;
+// Memory that a call reads or writes: `rows` rows of `width` bytes, `pitch` bytes apart.
+struct Span {
+  const void* p;
+  int64_t rows, width, pitch;
+  bool may_be_out0 = false;  // an input that the call's first output may be (same matrix): each element
+                             // is read before it is written, by one thread
+};
+inline Span mat_span(const void* p, int64_t rows, int64_t cols, int64_t ld, int es, bool may_be_out0 = false) {
+  return Span{p, rows, cols * es, ld * es, may_be_out0};
 }
-// May an output at `a` share memory with an input at `b`?  Yes when they are the same matrix
-// (one thread reads an element before it writes it) or do not meet.
-inline bool alias_ok(const void* a, int64_t lda, uint64_t na, const void* b, int64_t ldb, uint64_t nb,
-                     bool same_ok) {
-  if (!a || !b || !na || !nb) return true;
-  if (a == b && lda == ldb && same_ok) return true;
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x + na <= y || y + nb <= x;
+inline Span vec_span(const void* p, int64_t n, int es) { return Span{p, 1, n * es, n * es}; }
+// Do two spans share no byte?  Either one ends before the other begins, or they are columns side by
+// side of rows of the same pitch.
+inline bool spans_apart(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return true;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  const uint64_t na = (uint64_t)(a.rows - 1) * a.pitch + a.width, nb = (uint64_t)(b.rows - 1) * b.pitch + b.width;
+  if (x + na <= y || y + nb <= x) return true;
+  const int64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+  if (b.rows > 1 && b.pitch != pitch) return false;
+  const int64_t off = y >= x ? (int64_t)((y - x) % pitch) : (int64_t)((pitch - (x - y) % pitch) % pitch);
+  return off >= a.width && off + b.width <= pitch;  // b's columns within a's gaps
+}
+// No output meets an input or another output, but that the first one may be an input that says so.
+inline bool outputs_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  const Span* o0 = outs.begin();
+  for (const Span* o = o0; o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (!(o == o0 && i.may_be_out0 && o->p == i.p && o->pitch == i.pitch) && !spans_apart(*o, i)) return false;
+    for (const Span* q = o0; q != o; ++q)
+      if (!spans_apart(*o, *q)) return false;
+  }
+  return true;
 }
 // Allow a kernel `most` bytes of dynamic shared memory on the current device (set once per kernel,
 // always with the same value, and device: the call costs as much as a tenth of a short launch).
