@@ -447,7 +447,8 @@ typedef enum {
 } jenga_activation;
 
 /* jenga_linear_fwd -- y = act(x w^T + bias) + residual; one kernel, one rounding of y.
- *   x: bf16 [M, K];  w: bf16 [N, K];  both with 16-byte aligned rows (pitch a multiple of 8).
+ *   x: bf16 [M, K];  w: bf16 [N, K];  both with 16-byte aligned rows (pitch a multiple of 8; a
+ *   single row has any pitch).
  *   (Rows that start on 128-byte lines are the fastest: 98 against 118 us for 4096 x 4088 -> 4096.)
  *   bias: [N] of bias_dt, nullable.   residual: bf16 [M, N], nullable; may be y itself.
  *   y: bf16 [M, N].   pre: bf16 [M, N] out, nullable: the rounded x w^T + bias, which the

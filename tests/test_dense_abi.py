@@ -111,3 +111,14 @@ def test_the_same_matrix_and_columns_side_by_side_are_no_overlap(lib):
     assert ln_bwd(lib, dy=at(0), ldy=768, dres=off(0, 512), ldr=768, dx=off(0, 1024), ldd=768) == _lib.EWORKSPACE
     assert ln_bwd(lib, x=at(1), ldx=512, dg=off(1, 512), h=128, ldy=128, ldr=128, ldd=128) == _lib.EWORKSPACE
     assert ln_bwd(lib, x=at(1), ldx=512, dg=off(1, 516 + 256), h=128, ldy=128, ldr=128, ldd=128) == _lib.EINVAL
+
+
+def test_a_single_row_has_no_pitch(lib):
+    one = dict(M=1, K=521, ldx=521, ldw=528, dx=None, pre=at(3), lddw=521)
+    assert lin_bwd(lib, **one) == _lib.EWORKSPACE
+    assert lin_bwd(lib, M=64, N=1, K=521, ldx=528, ldw=521, ldd=521, lddw=521) == _lib.EWORKSPACE
+    assert lin_bwd(lib, **{**one, "M": 2}) == _lib.EINVAL  # two rows: the second is not 16-byte aligned
+    assert lin_bwd(lib, **{**one, "x": off(1, 2)}) == _lib.EINVAL
+    need = lib.jenga_linear_fwd_workspace_bytes(1, 256, 8193)  # split reduction: ends at the missing workspace
+    assert need > 0 and lin_fwd(lib, M=1, K=8193, ldx=8193, ldw=8200, w=at(16)) == _lib.EWORKSPACE
+    assert lin_fwd(lib, M=2, K=8193, ldx=8193, ldw=8200, w=at(16)) == _lib.EINVAL

@@ -211,3 +211,20 @@ def test_inputs_and_outputs_side_by_side_in_one_matrix(J):
     assert torch.equal(ln[:, K:], J.jenga_dropout(x0, 0.3, 5, 6)) and torch.equal(ln[:, :K], x0)
     assert torch.isnan(b[:, K + 2 * N:]).all()
     J.jenga_check_device_status()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 521), (1, 700, 8191), (40, 1, 521), (1, 1, 3), (300, 1, 77)])
+def test_linear_single_rows_of_any_length(J, M, N, K):
+    """One row of x, or of w, as it lies: its stride is no multiple of eight elements."""
+    P = (K + 7) // 8 * 8
+    x = randn(1, 1, K) if M == 1 else randn(1, M, P)[:, :K]
+    w = randn(2, 1, K, scale=0.1) if N == 1 else randn(2, N, P, scale=0.1)[:, :K]
+    dy = randn(3, M, N)
+    y, _ = J.jenga_linear_fwd(x, w)
+    dx, dw, db = J.jenga_linear_bwd(dy, x, w)
+    J.jenga_check_device_status()
+    X, W, D = x.double(), w.double(), dy.double()
+    close(y, X @ W.T, 2 * (K + 4) * U * (X.abs() @ W.abs().T) + RB * (X @ W.T).abs() * 1.001)
+    close(dx, D @ W, 2 * (N + 4) * U * (D.abs() @ W.abs()) + RB * (D @ W).abs() * 1.001 + 1e-30)
+    close(dw, D.T @ X, 2 * (M + 4) * U * (D.abs().T @ X.abs()) + 1e-30)
+    close(db, D.sum(0), (M + 4) * U * D.abs().sum(0) + 1e-30)

@@ -413,6 +413,8 @@ static jenga_status lin_out(const LinShape& s, const void* x, int64_t ldx, const
 }
 
 static bool lin_operand_ok(const void* p, int64_t ld) { return is16(p) && ld % 8 == 0; }
+// the pitch of x or w: a single row has none, whatever the caller's stride says
+static int64_t lin_pitch(int64_t rows, int64_t ld) { return rows == 1 ? (ld + 7) / 8 * 8 : ld; }
 
 static int dz_rows_per(int M, int N) {  // rows per chunk of linear_dz: about four CTAs an SM, whole steps of 32
   const int strips = (N + 255) / 256;
@@ -487,6 +489,8 @@ extern "C" jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void*
                   "jenga_linear_fwd: row pitch smaller than the row");
   if (M == 0) return JENGA_OK;
   JENGA_CHECK_ARG(x && w && y, "jenga_linear_fwd: null pointer");
+  ldx = lin_pitch(M, ldx);
+  ldw = lin_pitch(N, ldw);
   JENGA_CHECK_ARG(lin_operand_ok(x, ldx) && lin_operand_ok(w, ldw),
                   "jenga_linear_fwd: x and w need 16-byte aligned rows (pitch a multiple of 8)");
   const auto apart = [&](size_t ws_used) {
@@ -572,6 +576,8 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
   }
   JENGA_CHECK_ARG(dy && (act == JENGA_ACT_NONE || pre) && (!dw || x) && (!dx || w), "jenga_linear_bwd: null pointer");
   if (!dx && !dw && !db) return JENGA_OK;
+  ldx = lin_pitch(M, ldx);
+  ldw = lin_pitch(N, ldw);
   JENGA_CHECK_ARG((!dw || lin_operand_ok(x, ldx)) && (!dx || lin_operand_ok(w, ldw)),
                   "jenga_linear_bwd: x and w need 16-byte aligned rows (pitch a multiple of 8)");
   if (act == JENGA_ACT_NONE) pre = nullptr;
