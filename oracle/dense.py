@@ -35,7 +35,7 @@ def layernorm_bwd(dy, x, mean, rstd, gamma=None):
 # ------------------------------------------------------------------ linear
 def act(z, kind):
     if kind == "relu":
-        return np.where(z > 0, z, 0.0)
+        return np.maximum(z, 0.0)  # keeps a NaN
     if kind == "gelu":
         return 0.5 * z * (1.0 + erf(z / math.sqrt(2.0)))
     if kind == "silu":

@@ -1,6 +1,7 @@
 """Host-side checks of the dense operators (no GPU): shapes of launches and refusals before any."""
 import ctypes
 
+import numpy as np
 import pytest
 
 from token_sparse_long_b200 import _lib
@@ -122,3 +123,9 @@ def test_a_single_row_has_no_pitch(lib):
     need = lib.jenga_linear_fwd_workspace_bytes(1, 256, 8193)  # split reduction: ends at the missing workspace
     assert need > 0 and lin_fwd(lib, M=1, K=8193, ldx=8193, ldw=8200, w=at(16)) == _lib.EWORKSPACE
     assert lin_fwd(lib, M=2, K=8193, ldx=8193, ldw=8200, w=at(16)) == _lib.EINVAL
+
+
+def test_oracle_relu_keeps_nan():
+    from oracle import dense as od
+    y = od.act(np.array([-1.0, 0.0, 2.0, np.nan, -np.inf, np.inf]), "relu")
+    assert np.array_equal(y, [0.0, 0.0, 2.0, np.nan, 0.0, np.inf], equal_nan=True)

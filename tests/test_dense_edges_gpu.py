@@ -228,3 +228,19 @@ def test_linear_single_rows_of_any_length(J, M, N, K):
     close(dx, D @ W, 2 * (N + 4) * U * (D.abs() @ W.abs()) + RB * (D @ W).abs() * 1.001 + 1e-30)
     close(dw, D.T @ X, 2 * (M + 4) * U * (D.abs().T @ X.abs()) + 1e-30)
     close(db, D.sum(0), (M + 4) * U * D.abs().sum(0) + 1e-30)
+
+
+@pytest.mark.parametrize("M", [1, 2, 16, 300])
+def test_relu_keeps_nan_and_infinity(J, M):
+    w = torch.zeros(72, 64, dtype=BF, device="cuda")
+    w[:, 0] = 1.0
+    x = torch.zeros(M, 64, dtype=BF, device="cuda")
+    for v, want in ((math.nan, math.nan), (math.inf, math.inf), (-math.inf, 0.0), (-3.0, 0.0), (2.0, 2.0)):
+        x[M - 1, 0] = v
+        b = torch.zeros(72, device="cuda")
+        y = J.jenga_linear_fwd(x, w, b, act="relu")[0][M - 1].float()
+        z = torch.full((72,), v, device="cuda")
+        assert torch.equal(torch.isnan(y), torch.isnan(z)), v
+        if not math.isnan(v):
+            assert (y == want).all(), v
+    J.jenga_check_device_status()
