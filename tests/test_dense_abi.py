@@ -129,3 +129,12 @@ def test_oracle_relu_keeps_nan():
     from oracle import dense as od
     y = od.act(np.array([-1.0, 0.0, 2.0, np.nan, -np.inf, np.inf]), "relu")
     assert np.array_equal(y, [0.0, 0.0, 2.0, np.nan, 0.0, np.inf], equal_nan=True)
+
+
+def test_workspace_of_sizes_that_are_refused(lib):
+    big = 2 ** 31 - 1
+    for M, N, K in ((big, 8, 8), (2 ** 30 + 1, 8, 8), (8, big, 8), (8, 8, big), (8, 2 ** 24 + 1, 8), (0, 8, 8), (8, -1, 8)):
+        assert lib.jenga_linear_fwd_workspace_bytes(M, N, K) == 0 and lib.jenga_linear_bwd_workspace_bytes(M, N, K, 2) == 0
+        assert lin_fwd(lib, M=M, N=N, K=K, ldx=K, ldw=K, ldr=N, ldy=N, ldp=N) in (0 if M == 0 else _lib.EINVAL, _lib.EINVAL)
+    assert lib.jenga_linear_bwd_workspace_bytes(2 ** 30, 8, 8, 2) >= 3 * 2 * 2 ** 30 * 64
+    assert lib.jenga_layernorm_bwd_workspace_bytes(big, 8) > 0 and lib.jenga_layernorm_bwd_workspace_bytes(big, 16385) == 0

@@ -461,10 +461,10 @@ static LinBwdWs lin_bwd_carve(void* ws, int M, int N, int K, int act) {
   return w;
 }
 
+static bool lin_sizes_ok(int M, int N, int K) { return M <= (1 << 30) && N <= (1 << 24) && K <= (1 << 24); }
 static jenga_status lin_check(const char* who, int M, int N, int K, const int32_t* n_kept, int blk, int act) {
   JENGA_CHECK_ARG(M >= 0 && N >= 1 && K >= 1 && blk >= 1, "%s: bad sizes M=%d N=%d K=%d blk=%d", who, M, N, K, blk);
-  JENGA_CHECK_ARG(M <= (1 << 30) && N <= (1 << 24) && K <= (1 << 24), "%s: sizes too large M=%d N=%d K=%d", who, M, N,
-                  K);
+  JENGA_CHECK_ARG(lin_sizes_ok(M, N, K), "%s: sizes too large M=%d N=%d K=%d", who, M, N, K);
   JENGA_CHECK_ARG(!n_kept || M % blk == 0, "%s: M (%d) must be whole blocks of %d", who, M, blk);
   JENGA_CHECK_ARG(act >= JENGA_ACT_NONE && act <= JENGA_ACT_SILU, "%s: activation %d", who, act);
   return JENGA_OK;
@@ -475,7 +475,7 @@ static jenga_status lin_check(const char* who, int M, int N, int K, const int32_
 using namespace jenga;
 
 extern "C" size_t jenga_linear_fwd_workspace_bytes(int M, int N, int K) {
-  if (M < 1 || N < 1 || K < 1) return 0;
+  if (M < 1 || N < 1 || K < 1 || !lin_sizes_ok(M, N, K)) return 0;
   return lin_rows_ok(M, K) ? 0 : lin_part_bytes(lin_shape(M, N, K), M, N);
 }
 
@@ -554,7 +554,7 @@ extern "C" jenga_status jenga_test_linear_rows_shape(int M, int K, int* warps_pe
 }
 
 extern "C" size_t jenga_linear_bwd_workspace_bytes(int M, int N, int K, jenga_activation act) {
-  if (M < 1 || N < 1 || K < 1) return 0;
+  if (M < 1 || N < 1 || K < 1 || !lin_sizes_ok(M, N, K)) return 0;
   return lin_bwd_carve(nullptr, M, N, K, act).bytes;
 }
 
