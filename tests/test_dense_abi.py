@@ -138,3 +138,20 @@ def test_workspace_of_sizes_that_are_refused(lib):
         assert lin_fwd(lib, M=M, N=N, K=K, ldx=K, ldw=K, ldr=N, ldy=N, ldp=N) in (0 if M == 0 else _lib.EINVAL, _lib.EINVAL)
     assert lib.jenga_linear_bwd_workspace_bytes(2 ** 30, 8, 8, 2) >= 3 * 2 * 2 ** 30 * 64
     assert lib.jenga_layernorm_bwd_workspace_bytes(big, 8) > 0 and lib.jenga_layernorm_bwd_workspace_bytes(big, 16385) == 0
+
+
+def test_binding_refuses_what_an_int_does_not_hold():
+    import torch
+    from token_sparse_long_b200 import api
+    m = lambda *s: torch.empty(*s, device="meta", dtype=torch.bfloat16)
+    big = 2 ** 31 - 1
+    assert api._mat(m(big, 1), "x") == 1 and api._mat(m(2, big), "x") == big
+    for shape in ((2 ** 31, 1), (2 ** 32 + 5, 1), (1, 2 ** 31), (2, 2 ** 32 + 8)):
+        with pytest.raises(ValueError):
+            api._mat(m(*shape), "x")
+    idx = torch.zeros(4096, dtype=torch.int32)
+    assert api._rows_arg(idx, None, 2 ** 19 - 1, None, 0) == 4096 * (2 ** 19 - 1)
+    assert api._rows_arg(None, None, 32, None, 640) == 640
+    for blk in (2 ** 20, 2 ** 32 + 32, 0, -1):
+        with pytest.raises(ValueError):
+            api._rows_arg(idx, None, blk, None, 0)

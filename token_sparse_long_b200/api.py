@@ -405,6 +405,9 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
 def _mat(t, name, cols=None, rows=None, dtype=None):
     """A 2-d tensor with contiguous rows; its pitch."""
     shape, st = t.shape, t.stride()
@@ -414,6 +417,8 @@ def _mat(t, name, cols=None, rows=None, dtype=None):
         raise ValueError(f"{name}: [{'>= ' + str(rows) if rows is not None else '*'}, {cols}] required, got {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: {dtype} required, got {t.dtype}")
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:  # ctypes would pass the low 32 bits
+        raise ValueError(f"{name}: {tuple(shape)}: at most 2^31 - 1 rows and columns")
     if shape[0] > 1:
         if st[0] < shape[1]:
             raise ValueError(f"{name}: rows overlap (strides {st})")
@@ -430,6 +435,8 @@ def _vec(t, name, n, dtype=None):
 
 def _rows_arg(idx, n_kept, blk, n_kept_max, rows):
     """Rows of a call: n_kept_max blocks with a block list, else `rows`."""
+    if not 1 <= blk <= _INT_MAX:
+        raise ValueError(f"blk: {blk} rows a block")
     for t, name in ((idx, "idx"), (n_kept, "n_kept")):
         if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
             raise ValueError(f"{name}: contiguous int32 required")
@@ -440,6 +447,8 @@ def _rows_arg(idx, n_kept, blk, n_kept_max, rows):
     n = idx.numel() if n_kept_max is None else int(n_kept_max)
     if n < 0 or n > idx.numel():
         raise ValueError(f"n_kept_max {n} of a list of {idx.numel()}")
+    if n * blk > _INT_MAX:
+        raise ValueError(f"{n} blocks of {blk} rows: at most 2^31 - 1 rows")
     return n * int(blk)
 
 
