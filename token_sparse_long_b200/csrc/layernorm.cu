@@ -528,24 +528,18 @@ __global__ void __launch_bounds__(MAXT)
     layernorm_bwd_kernel(const T* dy, int64_t ldy, const T* x, int64_t ldx, RowMap map, int h, int gw,
                          const float* mean, const float* rstd, const void* gamma, int wbf16, const T* dres,
                          int64_t ldr, T* dx, int64_t ldd, float* ws) {
-  constexpr int VEC = 1;
   extern __shared__ float s_dyn[];
   __shared__ float s_red[2][2][32];  // [parity][sum][warp of the CTA]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (blockDim.x >> 5) / gw, grp = warp / gw, gwarp = warp - grp * gw;
-  const int nvec = h / VEC, step = gw * 32, t0 = gwarp * 32 + lane;
+  const int step = gw * 32, t0 = gwarp * 32 + lane;
   const int valid = valid_rows(map);
   const int G = gridDim.x * groups;
-  float ga[NV][VEC], ag[NV][VEC], ab[NV][VEC];
+  float ga[NV], ag[NV], ab[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      ga[i][e] = 0.f;
-      ag[i][e] = 0.f;
-      ab[i][e] = 0.f;
-    }
-    if (t0 + i * step < nvec) load_params<VEC>(gamma, wbf16, (int64_t)(t0 + i * step) * VEC, 1.f, ga[i]);
+    ga[i] = ag[i] = ab[i] = 0.f;
+    if (t0 + i * step < h) load_params<1>(gamma, wbf16, t0 + i * step, 1.f, &ga[i]);
   }
   auto fetch = [&](BwdRow<T, NV>& b, int64_t r) {  // 64 bits: a row count near 2^31 plus a step
     b.row = -1;
@@ -559,10 +553,10 @@ __global__ void __launch_bounds__(MAXT)
     b.rstd = rstd[r];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(t0 + i * step) * VEC;
+      const int c = t0 + i * step;
       b.x[i].zero();
       b.dy[i].zero();
-      if (t0 + i * step < nvec) {
+      if (c < h) {
         b.x[i].load(x + b.row * ldx + c);
         b.dy[i].load(dy + r * ldy + c);
         if (RES) b.res[i].load(dres + b.row * ldr + c);
@@ -583,18 +577,15 @@ __global__ void __launch_bounds__(MAXT)
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float xf[VEC], df[VEC];
-        cur.x[i].get(xf);
-        cur.dy[i].get(df);
-        if (t0 + i * step < nvec) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float n = (xf[e] - cur.mean) * cur.rstd, g = df[e] * ga[i][e];
-            s1 += g;
-            s2 = fmaf(g, n, s2);
-            ag[i][e] = fmaf(df[e], n, ag[i][e]);
-            ab[i][e] += df[e];
-          }
+        float xf, df;
+        cur.x[i].get(&xf);
+        cur.dy[i].get(&df);
+        if (t0 + i * step < h) {
+          const float n = (xf - cur.mean) * cur.rstd, g = df * ga[i];
+          s1 += g;
+          s2 = fmaf(g, n, s2);
+          ag[i] = fmaf(df, n, ag[i]);
+          ab[i] += df;
         }
       }
       s1 = warp_sum(s1);
@@ -616,53 +607,33 @@ __global__ void __launch_bounds__(MAXT)
       const float c1 = s1 * inv_h, c2 = s2 * inv_h;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int64_t c = (int64_t)(t0 + i * step) * VEC;
-        if (t0 + i * step < nvec) {
-          float xf[VEC], df[VEC], rf[VEC], o[VEC];
-          cur.x[i].get(xf);
-          cur.dy[i].get(df);
-          if (RES) cur.res[i].get(rf);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float n = (xf[e] - cur.mean) * cur.rstd;
-            o[e] = cur.rstd * (fmaf(df[e], ga[i][e], -c1) - n * c2);
-            if (RES) o[e] += rf[e];
-          }
-          RowVec<T, VEC>::store(dx + cur.row * ldd + c, o);
+        if (t0 + i * step < h) {
+          float xf, df, rf, o;
+          cur.x[i].get(&xf);
+          cur.dy[i].get(&df);
+          if (RES) cur.res[i].get(&rf);
+          const float n = (xf - cur.mean) * cur.rstd;
+          o = cur.rstd * (fmaf(df, ga[i], -c1) - n * c2);
+          if (RES) o += rf;
+          RowVec<T, 1>::store(dx + cur.row * ldd + t0 + i * step, &o);
         }
       }
     }
     cur = nxt;
   }
   if (!ws) return;
+  // sums of the CTA: its one group's, or [group][2][h] in shared memory added in group order
   float* out = ws + (int64_t)blockIdx.x * 2 * h;
-  if (groups == 1) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(t0 + i * step) * VEC;
-      if (t0 + i * step < nvec) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          out[c + e] = ag[i][e];
-          out[h + c + e] = ab[i][e];
-        }
-      }
-    }
-    return;
-  }
-  // several groups: [group][2][h] in shared memory, added in group order
-  float* mine = s_dyn + (int64_t)grp * 2 * h;
+  float* mine = groups == 1 ? out : s_dyn + (int64_t)grp * 2 * h;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t)(t0 + i * step) * VEC;
-    if (t0 + i * step < nvec) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        mine[c + e] = ag[i][e];
-        mine[h + c + e] = ab[i][e];
-      }
+    const int c = t0 + i * step;
+    if (c < h) {
+      mine[c] = ag[i];
+      mine[h + c] = ab[i];
     }
   }
+  if (groups == 1) return;
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * h; c += blockDim.x) {
     float a = 0.f;
@@ -861,10 +832,13 @@ static cudaError_t ln_bwd_one(const LnShape& s, const LnBwdCall& c, cudaStream_t
     kernel<<<s.ctas, threads, s.smem, st>>>((const T*)c.dy, c.ldy, (const T*)c.x, c.ldx, c.map, c.h, s.gw, c.mean,
                                             c.rstd, c.gamma, c.wbf16, (const T*)c.dres, c.ldr, (T*)c.dx, c.ldd, c.part);
   };
-  if (threads <= 512)
-    c.dres ? go(layernorm_bwd_kernel<T, NV, true, 512>) : go(layernorm_bwd_kernel<T, NV, false, 512>);
-  else
-    c.dres ? go(layernorm_bwd_kernel<T, NV, true, 1024>) : go(layernorm_bwd_kernel<T, NV, false, 1024>);
+  if constexpr (NV == 16) {  // fewer elements a thread stay within 512 threads
+    if (threads > 512) {
+      c.dres ? go(layernorm_bwd_kernel<T, NV, true, 1024>) : go(layernorm_bwd_kernel<T, NV, false, 1024>);
+      return cudaSuccess;
+    }
+  }
+  c.dres ? go(layernorm_bwd_kernel<T, NV, true, 512>) : go(layernorm_bwd_kernel<T, NV, false, 512>);
   return cudaSuccess;
 }
 template <typename T>
