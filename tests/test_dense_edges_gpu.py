@@ -244,3 +244,39 @@ def test_relu_keeps_nan_and_infinity(J, M):
         if not math.isnan(v):
             assert (y == want).all(), v
     J.jenga_check_device_status()
+
+
+# ------------------------------------------------------------------ dw as an fp32 result
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("M,N,K", [(4096, 520, 264), (4096, 2304, 1024)])
+def test_linear_dw_holds_all_bits_of_a_smooth_dz(J, act, M, N, K):
+    """dw's error as a whole.  dz is within about 8 half steps of fp32 (its slope's evaluation) and held in
+    24 bits; 512 products a time lose 5e-7 in the truncating accumulator: together below 1.1e-6.
+    With dz in 16 bits it is 4e-6, and so it is with 4096 products in one accumulator."""
+    x, dy, z = randn(1, M, K), randn(2, M, N), randn(3, M, N)
+    dw = J.jenga_linear_bwd(dy, x, randn(4, N, K), act=act, pre=z, need=("dw",))[1]
+    J.jenga_check_device_status()
+    Z = z.double()
+    if act == "gelu":
+        P, f = _phi(Z)
+        dz = dy.double() * (P + Z * f)
+    else:
+        s = torch.sigmoid(Z)
+        dz = dy.double() * s * (1 + Z * (1 - s))
+    want = dz.T @ x.double()
+    assert float((dw.double() - want).norm() / want.norm()) < 1.5e-6
+
+
+@pytest.mark.parametrize("N,K", [(512, 256), (2304, 2304)])
+def test_linear_dw_of_many_positive_rows(J, N, K):
+    """All products positive, so truncation adds up.  512 of them enter an accumulator in 32 steps of 16;
+    a step truncates the aligned products and the sum, each by less than 2^-23 of the sum so far, half the
+    chunk's on average: 2 * 32 * 2^-23 / 2 = 3.8e-6; the chunks' sums are added with rounding, 32 half
+    steps of half the total: 1e-6.  In one accumulator 16384 rows would lose about 5e-5."""
+    M = 16384
+    x, dy = randn(1, M, K).abs() + 0.25, randn(2, M, N).abs() + 0.25
+    _, dw, db = J.jenga_linear_bwd(dy, x, randn(4, N, K), need=("dw", "db"))
+    J.jenga_check_device_status()
+    want = dy.double().T @ x.double()
+    assert float(((dw.double() - want) / want).abs().max()) < 4.9e-6
+    close(db, dy.double().sum(0), 200 * U * dy.double().sum(0))
