@@ -467,7 +467,8 @@ JENGA_API jenga_status jenga_linear_fwd(const void* x, int64_t ldx, const void* 
  *   dx: bf16 [M, K], nullable.   dw: fp32 [N, K] (pitch lddw), nullable.   db: fp32 [N], nullable.
  *   dw and db are added to when accumulate != 0, else overwritten.  x may be null without dw,
  *   w without dx; the two need 16-byte aligned rows as in the forward.
- *   ws: jenga_linear_bwd_workspace_bytes(M, N, K, act) bytes (dz, partial sums).
+ *   ws: jenga_linear_bwd_workspace_bytes(M, N, K, act) bytes (dz, partial sums; dz takes 2 M N
+ *   bytes, 6 M N for GELU and SiLU with dw: without dw the bytes of RELU are enough for them).
  * fp32 accumulation, promoted out of the tensor core's accumulator every 512 rows in dw; dz
  * enters the products as bf16 (exact for NONE and RELU), as three bf16 parts in dw for GELU
  * and SILU.  No atomics: repeated calls on one device give identical bits.

@@ -155,3 +155,15 @@ def test_binding_refuses_what_an_int_does_not_hold():
     for blk in (2 ** 20, 2 ** 32 + 32, 0, -1):
         with pytest.raises(ValueError):
             api._rows_arg(idx, None, blk, None, 0)
+
+
+def test_linear_bwd_workspace_without_dw(lib):
+    size = lambda act: lib.jenga_linear_bwd_workspace_bytes(26240, 11008, 4096, act)
+    assert size(2) - size(1) >= 2 * 2 * 26240 * 11008  # two more bf16 parts of dz, for dw alone
+    for act in (2, 3):
+        # the size is checked before the overlap: one byte short and then a workspace on dy
+        small = lib.jenga_linear_bwd_workspace_bytes(64, 256, 512, 1)
+        k = dict(act=act, dw=None, ws=at(0))
+        assert lin_bwd(lib, nws=small - 1, **k) == _lib.EWORKSPACE and lin_bwd(lib, nws=small, **k) == _lib.EINVAL
+        k["dw"] = at(5)
+        assert lin_bwd(lib, nws=small, **k) == _lib.EWORKSPACE

@@ -280,3 +280,16 @@ def test_linear_dw_of_many_positive_rows(J, N, K):
     want = dy.double().T @ x.double()
     assert float(((dw.double() - want) / want).abs().max()) < 4.9e-6
     close(db, dy.double().sum(0), 280 * U * dy.double().sum(0))
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_linear_bwd_without_dw_in_the_smaller_workspace(J, act):
+    M, N, K = 700, 328, 264
+    x, w, dy, z = randn(1, M, K), randn(2, N, K, scale=0.1), randn(3, M, N), randn(4, M, N)
+    full = J.jenga_linear_bwd(dy, x, w, act=act, pre=z)
+    n = J._lib.load().jenga_linear_bwd_workspace_bytes(M, N, K, J._lib.ACT_RELU)
+    buf = torch.full((n + 4096,), 170, dtype=torch.uint8, device="cuda")
+    dx, dw, db = J.jenga_linear_bwd(dy, x, w, act=act, pre=z, need=("dx", "db"), ws=buf[:n])
+    assert dw is None and torch.equal(dx, full[0]) and torch.equal(db, full[2])
+    assert (buf[n:] == 170).all()
+    J.jenga_check_device_status()

@@ -618,7 +618,8 @@ def jenga_linear_bwd(dy, x, w, act="none", pre=None, n_kept=None, blk=1, need=("
             _vec(db, "db", N, f32)
         lib, a = load(), ACTIVATIONS[act]
         if ws is None:
-            ws = x.new_empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, a), dtype=torch.uint8)
+            wa = a if want_w else min(a, _lib.ACT_RELU)  # dz's further parts are dw's
+            ws = x.new_empty(lib.jenga_linear_bwd_workspace_bytes(M, N, K, wa), dtype=torch.uint8)
         check(lib.jenga_linear_bwd(dy.data_ptr(), ldy, x.data_ptr(), ldx, w.data_ptr(), ldw, a, _ptr(pre), ldp, M, N, K,
                                    _ptr(n_kept), int(blk), _ptr(dx), ldd, _ptr(dw), lddw, _ptr(db), 1 if accumulate else 0,
                                    ws.data_ptr(), ws.numel(), s))

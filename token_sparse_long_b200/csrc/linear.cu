@@ -591,11 +591,13 @@ extern "C" jenga_status jenga_linear_bwd(const void* dy, int64_t ldy, const void
   };
   const char* met = "jenga_linear_bwd: an output or the workspace overlaps an input or another output";
   JENGA_CHECK_ARG(apart(0), "%s", met);
-  const size_t need = jenga_linear_bwd_workspace_bytes(M, N, K, act);
+  // without dw one bf16 copy of dz is all that is kept
+  const jenga_activation ws_act = dw || act == JENGA_ACT_NONE ? act : JENGA_ACT_RELU;
+  const size_t need = jenga_linear_bwd_workspace_bytes(M, N, K, ws_act);
   if (!ws || ws_bytes < need)
     return fail(JENGA_EWORKSPACE, "jenga_linear_bwd: workspace %zu < %zu", ws ? ws_bytes : (size_t)0, need);
   JENGA_CHECK_ARG(apart(need), "%s", met);
-  const LinBwdWs W = lin_bwd_carve(ws, M, N, K, act);
+  const LinBwdWs W = lin_bwd_carve(ws, M, N, K, ws_act);
   // dy itself is the operand when nothing has to be computed, aligned or cut off at a device count
   const bool direct = act == JENGA_ACT_NONE && !n_kept && lin_operand_ok(dy, ldy);
   const bf16* dz = direct ? (const bf16*)dy : W.dz;
