@@ -8,6 +8,8 @@ value (one rounding step).  Exact for results in the bf16 normal range and zero.
 """
 import numpy as np
 
+from .rows import by_rows
+
 _DROP = 45                      # float64 has 52 fraction bits, bf16 keeps 7
 _HALF = np.uint64((1 << (_DROP - 1)) - 1)
 _MASK = np.uint64(~((1 << _DROP) - 1) & 0xFFFFFFFFFFFFFFFF)
@@ -15,6 +17,12 @@ _MASK = np.uint64(~((1 << _DROP) - 1) & 0xFFFFFFFFFFFFFFFF)
 
 def round_bf16(x):
     """Round float64 values to the nearest bf16 value (ties to even); returns float64."""
+    if np.ndim(x) >= 2 and np.size(x):
+        return by_rows(_round_bf16, np.asarray(x, np.float64))
+    return _round_bf16(x)
+
+
+def _round_bf16(x):
     a = np.array(x, dtype=np.float64, copy=True)
     b = a.view(np.uint64)
     lsb = (b >> np.uint64(_DROP)) & np.uint64(1)
@@ -26,8 +34,12 @@ def round_bf16(x):
 
 def from_bits(u16):
     """bf16 bit patterns (uint16) -> float64 values (exact)."""
-    u = np.asarray(u16, dtype=np.uint16).astype(np.uint32) << 16
-    return u.view(np.float32).astype(np.float64)
+    u = np.asarray(u16, dtype=np.uint16)
+    return by_rows(_from_bits, u) if u.ndim >= 2 and u.size else _from_bits(u)
+
+
+def _from_bits(u):
+    return (u.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
 
 
 def round_f32(x):

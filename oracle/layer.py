@@ -44,6 +44,7 @@ import numpy as np
 
 from .bf16 import from_bits, round_bf16
 from .movement import retained_rows
+from .rows import by_rows
 
 
 @dataclass
@@ -87,17 +88,22 @@ def _r(x, rnd):
 
 def rms_norm(x, g, eps):
     """y = x / sqrt(mean(x^2) + eps) * g (per row); returns y and the row factor."""
-    rstd = 1.0 / np.sqrt((x * x).mean(axis=1) + eps)
-    return x * rstd[:, None] * g[None, :], rstd
+    def rows(x):
+        rstd = 1.0 / np.sqrt((x * x).mean(axis=1) + eps)
+        return x * rstd[:, None] * g[None, :], rstd
+    return by_rows(rows, x)
 
 
 def rms_norm_bwd(dy, x, g, rstd):
     """Gradient of ``rms_norm`` w.r.t. x (derived by hand):
     dx_j = r g_j dy_j - x_j r^3 / N * sum_i dy_i g_i x_i."""
     N = x.shape[1]
-    dyg = dy * g[None, :]
-    dot = (dyg * x).sum(axis=1)
-    return dyg * rstd[:, None] - x * (rstd ** 3 * dot / N)[:, None]
+
+    def rows(dy, x, rstd):
+        dyg = dy * g[None, :]
+        dot = (dyg * x).sum(axis=1)
+        return dyg * rstd[:, None] - x * (rstd ** 3 * dot / N)[:, None]
+    return by_rows(rows, dy, x, rstd)
 
 
 def rope_cos_sin(pos, D, theta):
@@ -110,17 +116,23 @@ def rope_cos_sin(pos, D, theta):
 def rope(x, cos, sin):
     """Rotate-half rotary embedding of x [n, H, D]."""
     half = x.shape[-1] // 2
-    x1, x2 = x[..., :half], x[..., half:]
-    c, s = cos[:, None, :], sin[:, None, :]
-    return np.concatenate([x1 * c - x2 * s, x2 * c + x1 * s], axis=-1)
+
+    def rows(x, cos, sin):
+        x1, x2 = x[..., :half], x[..., half:]
+        c, s = cos[:, None, :], sin[:, None, :]
+        return np.concatenate([x1 * c - x2 * s, x2 * c + x1 * s], axis=-1)
+    return by_rows(rows, x, cos, sin)
 
 
 def rope_bwd(dy, cos, sin):
     """Transpose of ``rope`` (rotation by the negative angle)."""
     half = dy.shape[-1] // 2
-    d1, d2 = dy[..., :half], dy[..., half:]
-    c, s = cos[:, None, :], sin[:, None, :]
-    return np.concatenate([d1 * c + d2 * s, d2 * c - d1 * s], axis=-1)
+
+    def rows(dy, cos, sin):
+        d1, d2 = dy[..., :half], dy[..., half:]
+        c, s = cos[:, None, :], sin[:, None, :]
+        return np.concatenate([d1 * c + d2 * s, d2 * c - d1 * s], axis=-1)
+    return by_rows(rows, dy, cos, sin)
 
 
 def sigmoid(z):
@@ -165,7 +177,7 @@ def _heads(t):
     return [np.ascontiguousarray(t[:, h]) for h in range(t.shape[1])]
 
 
-def attention_fwd(q, k, v, chunk=1024, pmap=map):
+def attention_fwd(q, k, v, chunk=256, pmap=map):
     """Causal softmax attention per head (softmax(q k^T / sqrt(D)) v, keys j <= i).
 
     Returns o [n, H, D] and the row log-sum-exp [H, n] of the scaled logits.  ``pmap``
@@ -211,7 +223,7 @@ def head_attention_bwd(args):
     return dq, dk, dv
 
 
-def attention_bwd(q, k, v, do, segments, chunk=1024, pmap=map):
+def attention_bwd(q, k, v, do, segments, chunk=256, pmap=map):
     """``head_attention_bwd`` for every head (mapped with ``pmap``): dq, dk, dv [n, H, D]."""
     dq = np.zeros_like(q)
     dk = np.zeros_like(q)
@@ -266,7 +278,7 @@ def layer_fwd(x, pos, W: Weights, rnd=True, pmap=map, mlp_keep=None):
     hn = _r(hn, rnd)
     gt = hn @ W.wg.T
     ut = hn @ W.wu.T
-    a = _r(silu(gt) * ut, rnd)
+    a = _r(by_rows(lambda g, u: silu(g) * u, gt, ut), rnd)
     out = _r(h + a @ W.wd.T, rnd)
     if mlp_keep is not None:
         mlp_keep = np.asarray(mlp_keep, bool)
@@ -313,8 +325,7 @@ def layer_bwd(ctx, G, W: Weights, segment_tokens=None, pmap=map):
         Gm = Gs if keep is None else Gs * keep[sl][:, None]
         da = Gm @ W.wd
         gt, ut = ctx["gt"][sl], ctx["ut"][sl]
-        dut = da * silu(gt)
-        dgt = da * ut * silu_grad(gt)
+        dut, dgt = by_rows(lambda d, g, u: (d * silu(g), d * u * silu_grad(g)), da, gt, ut)
         dhn = dgt @ W.wg + dut @ W.wu
         dh_all[sl] = Gs + rms_norm_bwd(dhn, h[sl], W.g2, ctx["rstd2"][sl])
         # --- attention block: h = x + o Wo^T

@@ -1,0 +1,44 @@
+"""Row-local functions on many rows.
+
+The oracle's element-wise and per-row steps (norms, rotary embedding, activations, bf16
+rounding) touch gigabytes of float64 at full workload sizes.  Taken a chunk of rows at a time
+their temporaries stay in cache, and numpy releases the interpreter while it computes, so the chunks
+run on all cores.  A row's result does not depend on the chunk it is in: the bits are those
+of the plain call.
+"""
+import os
+from concurrent.futures import ThreadPoolExecutor
+
+import numpy as np
+
+CHUNK_BYTES = 1 << 21
+
+_pool = None
+
+
+def _threads():
+    global _pool
+    if _pool is None or _pool[0] != os.getpid():
+        n = len(os.sched_getaffinity(0)) if hasattr(os, "sched_getaffinity") else os.cpu_count() or 1
+        _pool = (os.getpid(), ThreadPoolExecutor(n))
+    return _pool[1]
+
+
+def by_rows(f, *arrays):
+    """f(*arrays) for an f that treats each row (first index, shared by all arrays) on its own
+    and returns an array with as many rows, or a tuple of them."""
+    n = len(arrays[0])
+    step = max(1, CHUNK_BYTES // max(1, arrays[0][:1].nbytes))
+    if n <= 4 * step:
+        return f(*arrays)
+    first = f(*(a[:step] for a in arrays))
+    firsts = first if isinstance(first, tuple) else (first,)
+    outs = [np.empty((n,) + o.shape[1:], o.dtype) for o in firsts]
+
+    def put(i, res):
+        for o, r in zip(outs, res if isinstance(res, tuple) else (res,)):
+            o[i:i + step] = r
+
+    put(0, first)
+    list(_threads().map(lambda i: put(i, f(*(a[i:i + step] for a in arrays))), range(step, n, step)))
+    return tuple(outs) if isinstance(first, tuple) else outs[0]

@@ -53,7 +53,7 @@ def head_column_mass(args):
     return mass
 
 
-def column_mass(q, k, causal=True, chunk=512, pmap=map):
+def column_mass(q, k, causal=True, chunk=256, pmap=map):
     """Per-key softmax column mass, summed over heads (in head order).
 
     q, k: [S, H, D].  Returns [S] with mass[j] = sum_h sum_i P^h_ij (``head_column_mass``
