@@ -44,7 +44,7 @@ import numpy as np
 
 from .bf16 import from_bits, round_bf16
 from .movement import retained_rows
-from .rows import by_rows
+from .rows import by_rows, one_blas_thread_in_a_worker
 
 
 @dataclass
@@ -154,6 +154,7 @@ def head_attention_fwd(args):
 
     o_i = softmax_j(q_i . k_j / sqrt(D)) v over keys j <= i.  Returns o [n, D] and the
     row log-sum-exp [n] of the scaled logits; rows go in chunks only to bound memory."""
+    one_blas_thread_in_a_worker()
     qh, kh, vh, chunk = args
     n, D = qh.shape
     scale = 1.0 / np.sqrt(D)
@@ -199,6 +200,7 @@ def head_attention_bwd(args):
     value gradients of keys [0, r1).  Per chunk, the textbook softmax-attention backward:
     P = softmax(q k^T / sqrt(D)) (causal), dP = dO V^T, dS = P * (dP - rowsum(P * dP)),
     dQ = dS K / sqrt(D), dK += dS^T Q / sqrt(D), dV += P^T dO.  Returns dq, dk, dv [n, D]."""
+    one_blas_thread_in_a_worker()
     qh, kh, vh, doh, segments, chunk = args
     n, D = qh.shape
     scale = 1.0 / np.sqrt(D)

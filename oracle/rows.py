@@ -6,6 +6,7 @@ their temporaries stay in cache, and numpy releases the interpreter while it com
 run on all cores.  A row's result does not depend on the chunk it is in: the bits are those
 of the plain call.
 """
+import multiprocessing
 import os
 from concurrent.futures import ThreadPoolExecutor
 
@@ -14,6 +15,22 @@ import numpy as np
 CHUNK_BYTES = 1 << 21
 
 _pool = None
+_one_thread_pid = None
+
+
+def one_blas_thread_in_a_worker():
+    """In a process-pool worker, BLAS takes one thread: the pool has a worker per core.  To be called
+    by the work itself, since a limit set when the worker starts, before numpy is loaded, finds no
+    BLAS to limit (16 workers of 16 threads each took five times as long on 16 cores)."""
+    global _one_thread_pid
+    if _one_thread_pid == os.getpid() or multiprocessing.parent_process() is None:
+        return
+    _one_thread_pid = os.getpid()
+    try:
+        from threadpoolctl import threadpool_limits
+    except ImportError:
+        return
+    threadpool_limits(1)
 
 
 def _threads():

@@ -20,6 +20,8 @@ query blocks that have at least one causal entry in column n.
 """
 import numpy as np
 
+from .rows import one_blas_thread_in_a_worker
+
 
 def _as_f64(a):
     return np.asarray(a, dtype=np.float64)
@@ -33,6 +35,7 @@ def head_column_mass(args):
     exponentiate, divide by the row sum); rows are processed in chunks only to bound
     memory, and a causal chunk of rows [i0, i1) only forms the keys j < i1 (the others
     have probability exactly 0)."""
+    one_blas_thread_in_a_worker()
     qh, kh, causal, chunk = args
     qh = _as_f64(qh)
     kh = _as_f64(kh)

@@ -4,6 +4,7 @@ import pytest
 
 from oracle import bf16, layer
 from oracle.rows import CHUNK_BYTES, by_rows
+from tests.oracle_pool import oracle_pool
 
 
 @pytest.mark.parametrize("n", [0, 1, 5, 700, 3001])
@@ -34,3 +35,19 @@ def test_an_exception_in_a_chunk_reaches_the_caller():
     x = np.repeat(np.arange(1000.0)[:, None], 5000, axis=1)
     with pytest.raises(ArithmeticError):
         by_rows(f, x)
+
+
+def _blas_threads(args):
+    from oracle import layer as oly
+    if args is not None:
+        oly.head_attention_fwd(args)
+    from threadpoolctl import threadpool_info
+    return max((i["num_threads"] for i in threadpool_info() if i.get("user_api") == "blas"), default=0)
+
+
+def test_pool_workers_run_blas_on_one_thread():
+    x = np.ones((8, 4))
+    before = _blas_threads(None)
+    with oracle_pool(2) as pmap:
+        assert set(pmap(_blas_threads, [(x, x, x, 4)] * 4)) == {1}
+    assert _blas_threads((x, x, x, 4)) == before  # and the caller's own BLAS keeps its threads
