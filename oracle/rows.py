@@ -21,7 +21,7 @@ _one_thread_pid = None
 def one_blas_thread_in_a_worker():
     """In a process-pool worker, BLAS takes one thread: the pool has a worker per core.  To be called
     by the work itself, since a limit set when the worker starts, before numpy is loaded, finds no
-    BLAS to limit (16 workers of 16 threads each took five times as long on 16 cores)."""
+    BLAS to limit (16 workers of 16 threads each on 16 cores took two to five times as long)."""
     global _one_thread_pid
     if _one_thread_pid == os.getpid() or multiprocessing.parent_process() is None:
         return
