@@ -152,12 +152,35 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t phase) { return poll_wait(bar, phase, SITE_LINEAR); }
 
-// ---- activations (fp32).  GELU takes the normal distribution from erfc: 1 + erf(z / sqrt 2) cancels for
-// negative z (nothing of it is left below -5.5).  __expf is within 2 + 1.17 |x| ulp, at most
+// ---- activations (fp32).  GELU takes the normal distribution's tail by itself: 1 + erf(z / sqrt 2) cancels
+// for negative z (nothing of it is left below -5.5).  __expf is within 2 + 1.17 |x| ulp, at most
 // 2^-16 relative: below a bf16 result's half step; the fp32 gradients dw and db carry it.
+//
+// P(Z > t) of a standard normal Z, t >= 0, and e = e^(-t^2/2): e times a polynomial of degree 9 in r =
+// 1 / (1 + 0.34 t) without a constant term (the ratio falls like 1 / t), a Lawson IRLS minimax fit of
+// its relative error on [0, 14], 3.2e-8; evaluated in fp32 with e within 0.7 (1.3 (1 + t^2) + 12)
+// half steps.  (erfcf instead: 4096 x 4096 -> 11008 with GELU 34 us longer.)
+__device__ __forceinline__ float normal_tail(float t, float& e) {
+  const float r = __fdividef(1.f, fmaf(0.34f, t, 1.f));
+  float a = -0x1.abf520p-6f;
+  a = fmaf(a, r, 0x1.1db1dcp-3f);
+  a = fmaf(a, r, -0x1.17b00ep-2f);
+  a = fmaf(a, r, 0x1.9e11d4p-3f);
+  a = fmaf(a, r, -0x1.6e5512p-5f);
+  a = fmaf(a, r, 0x1.d882c8p-4f);
+  a = fmaf(a, r, 0x1.d7d984p-4f);
+  a = fmaf(a, r, 0x1.16c1fep-3f);
+  a = fmaf(a, r, 0x1.15c034p-3f);
+  e = fast_exp2(t * t * -0.72134752044448170f);
+  return a * r * e;
+}
 __device__ __forceinline__ float act_value(float z, int act) {
   if (act == JENGA_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-  if (act == JENGA_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678118654752f);
+  if (act == JENGA_ACT_GELU) {
+    float e;
+    const float q = normal_tail(fabsf(z), e);
+    return z * (z < 0.f ? q : 1.f - q);
+  }
   if (act == JENGA_ACT_SILU) return z / (1.f + __expf(-z));
   return z;
 }
@@ -178,8 +201,11 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   if (act == JENGA_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   // a pre-activation beyond bf16's range is saved as an infinity: the slopes' limits
   if (act != JENGA_ACT_NONE && fabsf(z) == INFINITY) return z > 0.f ? 1.f : 0.f;
-  if (act == JENGA_ACT_GELU)
-    return 0.5f * erfcf(z * -0.70710678118654752f) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+  if (act == JENGA_ACT_GELU) {
+    float e;
+    const float q = normal_tail(fabsf(z), e);
+    return fmaf(z * 0.39894228040143268f, e, z < 0.f ? q : 1.f - q);
+  }
   if (act == JENGA_ACT_SILU) {
     const float s = 1.f / (1.f + __expf(-z));
     return s * (1.f + z * (1.f - s));
