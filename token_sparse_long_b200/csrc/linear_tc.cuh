@@ -159,7 +159,7 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t phase) { retur
 // P(Z > t) of a standard normal Z, t >= 0, and e = e^(-t^2/2): e times a polynomial of degree 9 in r =
 // 1 / (1 + 0.34 t) without a constant term (the ratio falls like 1 / t), a Lawson IRLS minimax fit of
 // its relative error on [0, 14], 3.2e-8; evaluated in fp32 with e within 0.7 (1.3 (1 + t^2) + 12)
-// half steps.  (erfcf instead: 4096 x 4096 -> 11008 with GELU 34 us longer.)
+// half steps.  (4096 x 4096 -> 11008 with GELU, pre-activation saved: 307 us, with erfcf 338.)
 __device__ __forceinline__ float normal_tail(float t, float& e) {
   const float r = __fdividef(1.f, fmaf(0.34f, t, 1.f));
   float a = -0x1.abf520p-6f;
