@@ -426,9 +426,11 @@ def cpu_baseline_one_thread():
     built before the clock starts."""
     from threadpoolctl import threadpool_limits
     from oracle import movement as omv
+    from oracle import rows as orows
     from oracle import scores as osc
     from oracle import select as osel
     out = {}
+    orows.THREADS = 1  # and so without its threads over row chunks
     with threadpool_limits(1):
         c = synth.gen_score_case(0)
         q = c.q.reshape(c.S, c.H, c.D).astype(np.float64)

@@ -13,6 +13,7 @@ from concurrent.futures import ThreadPoolExecutor
 import numpy as np
 
 CHUNK_BYTES = 1 << 21
+THREADS = None  # of by_rows; None: one per core (the one-thread timing sets 1)
 
 _pool = None
 _one_thread_pid = None
@@ -35,9 +36,9 @@ def one_blas_thread_in_a_worker():
 
 def _threads():
     global _pool
-    if _pool is None or _pool[0] != os.getpid():
-        n = len(os.sched_getaffinity(0)) if hasattr(os, "sched_getaffinity") else os.cpu_count() or 1
-        _pool = (os.getpid(), ThreadPoolExecutor(n))
+    n = THREADS or (len(os.sched_getaffinity(0)) if hasattr(os, "sched_getaffinity") else os.cpu_count() or 1)
+    if _pool is None or _pool[0] != (os.getpid(), n):
+        _pool = ((os.getpid(), n), ThreadPoolExecutor(n))
     return _pool[1]
 
 
@@ -57,5 +58,6 @@ def by_rows(f, *arrays):
             o[i:i + step] = r
 
     put(0, first)
-    list(_threads().map(lambda i: put(i, f(*(a[i:i + step] for a in arrays))), range(step, n, step)))
+    run = map if THREADS == 1 else _threads().map
+    list(run(lambda i: put(i, f(*(a[i:i + step] for a in arrays))), range(step, n, step)))
     return tuple(outs) if isinstance(first, tuple) else outs[0]

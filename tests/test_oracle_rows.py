@@ -51,3 +51,20 @@ def test_pool_workers_run_blas_on_one_thread():
     with oracle_pool(2) as pmap:
         assert set(pmap(_blas_threads, [(x, x, x, 4)] * 4)) == {1}
     assert _blas_threads((x, x, x, 4)) == before  # and the caller's own BLAS keeps its threads
+
+
+def test_one_thread_on_request(monkeypatch):
+    import threading
+
+    from oracle import rows
+    seen = set()
+
+    def f(a):
+        seen.add(threading.get_ident())
+        return a + 1
+    x = np.zeros((4000, 1000))
+    monkeypatch.setattr(rows, "THREADS", 1)
+    assert (by_rows(f, x) == 1).all() and seen == {threading.get_ident()}
+    monkeypatch.setattr(rows, "THREADS", 3)
+    seen.clear()
+    assert (by_rows(f, x) == 1).all() and 1 < len(seen) <= 4
